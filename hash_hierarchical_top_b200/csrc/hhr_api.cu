@@ -9,10 +9,13 @@
 
 #include "../../include/hhr.h"
 #include "attn.cuh"
+#include "block_select.cuh"
 #include "common.cuh"
 #include "encode.cuh"
 #include "encode_tc.cuh"
 #include "indexer.cuh"
+#include "kv8.cuh"
+#include "paged_attn.cuh"
 #include "row_cluster.cuh"
 #include "select.cuh"
 #include "step.cuh"
@@ -944,6 +947,272 @@ int hhr_read_device_status(void* stream, int* bits) {
   }
   if (bits != nullptr) *bits = v;
   return v == 0 ? HHR_OK : HHR_ERR_DEVICE_STATUS;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// The 8-bit cache, dense paged attention and block-sparse attention.
+
+namespace {
+
+bool g_smem_topm[kMaxDevices];
+
+// Cache rows are addressed with 32-bit row indices.
+bool rows_fit(const hhr_dims* d) {
+  return (unsigned long long)d->n_phys_pages * d->n_kv_heads * d->page_size < 0xffffffffull;
+}
+
+// The four arrays of an 8-bit cache.
+int check_kv8(const hhr_dims* d, const uint8_t* k, const uint8_t* v, const uint8_t* k_exp,
+              const uint8_t* v_exp) {
+  if (k == nullptr || v == nullptr || k_exp == nullptr || v_exp == nullptr)
+    return HHR_ERR_INVALID_ARG;
+  if (misaligned16({k, v, k_exp, v_exp})) return HHR_ERR_INVALID_ARG;
+  return rows_fit(d) ? HHR_OK : HHR_ERR_UNSUPPORTED;
+}
+
+constexpr int kMaxListBlocks = 32768;  // blocks per list
+// Dynamic shared memory that needs no opt-in, beside a few KB of static shared memory.
+constexpr size_t kDefaultSmem = 36 * 1024;
+
+// CTAs of a page attention over at most `units` units of work, and the bytes of their partials
+// (two per CTA).
+int page_ctas(long long units) {
+  const long long n = (long long)kPaCtasPerSm * sm_count();
+  return (int)(units < n ? units : n);
+}
+long long page_units(const hhr_dims* d, int T, int blocks) {
+  const long long u = ((long long)blocks * d->page_size + kUnitKeys - 1) / kUnitKeys;
+  return (long long)d->batch * T * sel_rows(d) * u;
+}
+size_t page_ws(const hhr_dims* d, int n_ctas) {
+  const size_t gs = d->n_q_heads / sel_rows(d);
+  return align256((size_t)2 * n_ctas * gs * kD * 4) + align256((size_t)2 * n_ctas * gs * 2 * 4);
+}
+
+// Launches the page attention and, where CTAs can share a row, the join of its partials.
+template <bool kList>
+int launch_page_attn(const hhr_dims* d, PageAttnArgs& a, bool k8, long long units, void* workspace,
+                     cudaStream_t s) {
+  a.B = d->batch; a.Hq = d->n_q_heads; a.G = d->n_kv_heads; a.Gs = sel_rows(d);
+  a.kv_div = kv_div(d); a.P = d->page_size; a.maxp = d->max_pages_per_seq;
+  a.n_phys = d->n_phys_pages;
+  a.p_mul = (uint32_t)((0x100000000ull + (unsigned)a.P - 1) / (unsigned)a.P);
+  a.n_ctas = page_ctas(units);
+  const size_t gs = a.Hq / a.Gs;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                       align256((size_t)2 * a.n_ctas * gs * kD * 4));
+  void (*k)(PageAttnArgs) = k8 ? page_attn_kernel<true, kList> : page_attn_kernel<false, kList>;
+  prof_begin(HHR_KERNEL_PAGE, s);
+  k<<<a.n_ctas, kPaThreads, page_attn_smem(), s>>>(a);
+  prof_end(HHR_KERNEL_PAGE, s);
+  int st = launch_status();
+  if (st != HHR_OK) return st;
+  prof_begin(HHR_KERNEL_JOIN, s);
+  const cudaError_t e = launch_pdl(page_join_kernel<kList>, dim3((unsigned)(a.B * a.T * a.Gs)),
+                                   dim3(kJoinThreads), 0, s, a);
+  prof_end(HHR_KERNEL_JOIN, s);
+  if (e != cudaSuccess) { g_last_cuda = e; return HHR_ERR_CUDA; }
+  return HHR_OK;
+}
+
+// What the two page attentions check alike: the cache, the scale and the output.
+int check_page_attn(const hhr_dims* d, const uint16_t* q, const void* k, const void* v,
+                    const uint8_t* k_exp, const uint8_t* v_exp, const int32_t* page_table,
+                    const int32_t* seq_len, float scale, const void* out, int out_bf16,
+                    const float* lse) {
+  if (q == nullptr || k == nullptr || v == nullptr || page_table == nullptr ||
+      seq_len == nullptr || out == nullptr)
+    return HHR_ERR_INVALID_ARG;
+  if ((k_exp == nullptr) != (v_exp == nullptr)) return HHR_ERR_INVALID_ARG;
+  if (!(scale == scale) || isinf(scale)) return HHR_ERR_INVALID_ARG;
+  if (out_bf16 != 0 && out_bf16 != 1) return HHR_ERR_INVALID_ARG;
+  if (misaligned16({q, k, v, k_exp, v_exp, out, lse})) return HHR_ERR_INVALID_ARG;
+  return rows_fit(d) ? HHR_OK : HHR_ERR_UNSUPPORTED;
+}
+
+// Dims and sizes of a query chunk.
+int check_chunk(const hhr_dims* d, int n_queries) {
+  int st = check_dims(d);
+  if (st != HHR_OK) return st;
+  if ((st = check_group(d)) != HHR_OK) return st;
+  if (n_queries < 1) return HHR_ERR_INVALID_ARG;
+  const long long rows = (long long)d->batch * n_queries * d->n_q_heads;
+  return rows > 0x7fffffffLL ? HHR_ERR_UNSUPPORTED : HHR_OK;
+}
+int check_dense(const hhr_dims* d) {
+  int st = check_dims(d);
+  if (st != HHR_OK) return st;
+  if ((st = check_group(d)) != HHR_OK) return st;
+  if (d->select_per_head) return HHR_ERR_INVALID_ARG;  // nothing is selected
+  return page_units(d, 1, d->max_pages_per_seq) > 0x7fffffffLL ? HHR_ERR_UNSUPPORTED : HHR_OK;
+}
+int check_list(const hhr_dims* d, int n_queries, int m_max) {
+  int st = check_chunk(d, n_queries);
+  if (st != HHR_OK) return st;
+  if (m_max < 1) return HHR_ERR_INVALID_ARG;
+  if (m_max > kMaxListBlocks) return HHR_ERR_UNSUPPORTED;
+  return page_units(d, n_queries, m_max) > 0x7fffffffLL ? HHR_ERR_UNSUPPORTED : HHR_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int hhr_append_kv8(const hhr_dims* d, const uint16_t* k_new, const uint16_t* v_new,
+                   int64_t token_stride, const int32_t* start, const int32_t* n_new, int max_new,
+                   const int32_t* page_table, uint8_t* k, uint8_t* v, uint8_t* k_exp,
+                   uint8_t* v_exp, float* block_mean, void* stream) {
+  int st = check_dims(d);
+  if (st != HHR_OK) return st;
+  if (k_new == nullptr || v_new == nullptr || start == nullptr || n_new == nullptr ||
+      page_table == nullptr || max_new < 0)
+    return HHR_ERR_INVALID_ARG;
+  if ((st = check_kv8(d, k, v, k_exp, v_exp)) != HHR_OK) return st;
+  if (token_stride < (int64_t)d->n_kv_heads * kD || token_stride % 8 != 0)
+    return HHR_ERR_INVALID_ARG;
+  if (misaligned16({k_new, v_new, block_mean})) return HHR_ERR_INVALID_ARG;
+  if (max_new == 0) return HHR_OK;
+  const long long pages = (max_new + (long long)d->page_size - 1) / d->page_size + 1;
+  AppendArgs a{k_new, v_new, start, n_new, page_table, k, v, k_exp, v_exp, block_mean,
+               token_stride, d->n_kv_heads, d->page_size, d->max_pages_per_seq, d->n_phys_pages,
+               max_new};
+  const dim3 grid((unsigned)pages, d->n_kv_heads, d->batch);
+  cudaStream_t s = (cudaStream_t)stream;
+  prof_begin(HHR_KERNEL_APPEND, s);
+  if (block_mean != nullptr)
+    append_kv8_kernel<true><<<grid, kAppendThreads, 0, s>>>(a);
+  else
+    append_kv8_kernel<false><<<grid, kAppendThreads, 0, s>>>(a);
+  prof_end(HHR_KERNEL_APPEND, s);
+  return launch_status();
+}
+
+int hhr_read_kv8(const hhr_dims* d, const uint8_t* k, const uint8_t* v, const uint8_t* k_exp,
+                 const uint8_t* v_exp, const int32_t* page_table, const int32_t* start,
+                 const int32_t* n, int max_n, uint16_t* k_out, uint16_t* v_out, void* stream) {
+  int st = check_dims(d);
+  if (st != HHR_OK) return st;
+  if (page_table == nullptr || start == nullptr || n == nullptr || k_out == nullptr ||
+      v_out == nullptr || max_n < 0)
+    return HHR_ERR_INVALID_ARG;
+  if ((st = check_kv8(d, k, v, k_exp, v_exp)) != HHR_OK) return st;
+  if (misaligned16({k_out, v_out})) return HHR_ERR_INVALID_ARG;
+  if (max_n == 0) return HHR_OK;
+  ReadArgs a{k, v, k_exp, v_exp, page_table, start, n, k_out, v_out, d->n_kv_heads, d->page_size,
+             d->max_pages_per_seq, d->n_phys_pages, max_n};
+  cudaStream_t s = (cudaStream_t)stream;
+  prof_begin(HHR_KERNEL_READ, s);
+  read_kv8_kernel<<<dim3((unsigned)((max_n + (long long)kReadRows - 1) / kReadRows),
+                         d->n_kv_heads, d->batch),
+                    kReadThreads, 0, s>>>(a);
+  prof_end(HHR_KERNEL_READ, s);
+  return launch_status();
+}
+
+size_t hhr_paged_attn_workspace_bytes(const hhr_dims* d) {
+  if (check_dense(d) != HHR_OK) return 0;
+  return page_ws(d, page_ctas(page_units(d, 1, d->max_pages_per_seq)));
+}
+
+int hhr_paged_attn(const hhr_dims* d, const uint16_t* q, const uint16_t* k_new,
+                   const uint16_t* v_new, void* k_cache, void* v_cache, uint8_t* k_exp,
+                   uint8_t* v_exp, const int32_t* page_table, const int32_t* seq_len, float scale,
+                   void* out, int out_bf16, float* lse, void* workspace, size_t ws_bytes,
+                   void* stream) {
+  int st = check_dense(d);
+  if (st != HHR_OK) return st;
+  if ((st = check_page_attn(d, q, k_cache, v_cache, k_exp, v_exp, page_table, seq_len, scale, out,
+                            out_bf16, lse)) != HHR_OK)
+    return st;
+  if ((k_new == nullptr) != (v_new == nullptr) || misaligned16({k_new, v_new}))
+    return HHR_ERR_INVALID_ARG;
+  if (workspace == nullptr) return HHR_ERR_INVALID_ARG;
+  const long long units = page_units(d, 1, d->max_pages_per_seq);
+  if (ws_bytes < page_ws(d, page_ctas(units))) return HHR_ERR_WORKSPACE;
+  if (((uintptr_t)workspace & 255) != 0) return HHR_ERR_INVALID_ARG;
+  PageAttnArgs a{};
+  a.q = q; a.k_new = k_new; a.v_new = v_new; a.k = k_cache; a.v = v_cache;
+  a.k_exp = k_exp; a.v_exp = v_exp; a.page_table = page_table; a.seq_len = seq_len;
+  a.out = out; a.out_bf16 = out_bf16; a.lse = lse; a.scale_log2 = scale * 1.4426950408889634f;
+  a.T = 1;
+  return launch_page_attn<false>(d, a, k_exp != nullptr, units, workspace, (cudaStream_t)stream);
+}
+
+size_t hhr_block_select_workspace_bytes(const hhr_dims* d, int n_queries) {
+  if (check_chunk(d, n_queries) != HHR_OK) return 0;
+  return align256((size_t)d->batch * n_queries * sel_rows(d) * d->max_pages_per_seq * 4);
+}
+
+int hhr_block_select(const hhr_dims* d, int n_queries, const uint16_t* q, const int32_t* seq_len,
+                     const int32_t* q_pos, const int32_t* page_table, const float* block_mean,
+                     int m_pages, const hhr_select_opts* opts, int32_t* out_blocks,
+                     int32_t* out_count, void* workspace, size_t ws_bytes, void* stream) {
+  int st = check_chunk(d, n_queries);
+  if (st != HHR_OK) return st;
+  if (m_pages < 1) return HHR_ERR_INVALID_ARG;
+  int sink = 0, local = 0;
+  if ((st = read_opts(d, HHR_MODE_HASH, opts, m_pages, 0, &sink, &local)) != HHR_OK) return st;
+  if (q == nullptr || seq_len == nullptr || page_table == nullptr || block_mean == nullptr ||
+      out_blocks == nullptr || out_count == nullptr || workspace == nullptr)
+    return HHR_ERR_INVALID_ARG;
+  if (misaligned16({q, block_mean})) return HHR_ERR_INVALID_ARG;
+  if (ws_bytes < hhr_block_select_workspace_bytes(d, n_queries)) return HHR_ERR_WORKSPACE;
+  if (((uintptr_t)workspace & 255) != 0) return HHR_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  const int B = d->batch, Gs = sel_rows(d), maxp = d->max_pages_per_seq;
+  BlockSelectArgs a{q, seq_len, q_pos, page_table, block_mean, static_cast<float*>(workspace),
+                    out_blocks, out_count, B, n_queries, d->n_q_heads, d->n_kv_heads, Gs,
+                    kv_div(d), d->page_size, maxp, d->n_phys_pages, m_pages,
+                    kept_max(d, m_pages, 0), sink, local};
+  const size_t smem = (size_t)maxp * 4;
+  if (smem > kDefaultSmem && allow_smem(block_topm_kernel, smem, g_smem_topm) != cudaSuccess)
+    return HHR_ERR_CUDA;
+  prof_begin(HHR_KERNEL_MEAN, s);
+  block_mean_score_kernel<<<dim3((maxp + kBsPages - 1) / kBsPages, d->n_kv_heads, B), kBsThreads,
+                            0, s>>>(a);
+  prof_end(HHR_KERNEL_MEAN, s);
+  if ((st = launch_status()) != HHR_OK) return st;
+  prof_begin(HHR_KERNEL_TOPM, s);
+  const cudaError_t e = launch_pdl(block_topm_kernel, dim3((unsigned)(B * n_queries * Gs)),
+                                   dim3(kBsSelThreads), smem, s, a);
+  prof_end(HHR_KERNEL_TOPM, s);
+  if (e != cudaSuccess) { g_last_cuda = e; return HHR_ERR_CUDA; }
+  return HHR_OK;
+}
+
+size_t hhr_block_attn_workspace_bytes(const hhr_dims* d, int n_queries, int m_max) {
+  if (check_list(d, n_queries, m_max) != HHR_OK) return 0;
+  return page_ws(d, page_ctas(page_units(d, n_queries, m_max)));
+}
+
+int hhr_block_attn(const hhr_dims* d, int n_queries, const uint16_t* q, const void* k_cache,
+                   const void* v_cache, const uint8_t* k_exp, const uint8_t* v_exp,
+                   const int32_t* page_table, const int32_t* seq_len, const int32_t* q_pos,
+                   const int32_t* blocks, const int32_t* block_count, int m_max, float scale,
+                   void* out, int out_bf16, float* lse, void* workspace, size_t ws_bytes,
+                   void* stream) {
+  int st = check_list(d, n_queries, m_max);
+  if (st != HHR_OK) return st;
+  if ((st = check_page_attn(d, q, k_cache, v_cache, k_exp, v_exp, page_table, seq_len, scale, out,
+                            out_bf16, lse)) != HHR_OK)
+    return st;
+  if (blocks == nullptr || block_count == nullptr || workspace == nullptr)
+    return HHR_ERR_INVALID_ARG;
+  const long long units = page_units(d, n_queries, m_max);
+  if (ws_bytes < page_ws(d, page_ctas(units))) return HHR_ERR_WORKSPACE;
+  if (((uintptr_t)workspace & 255) != 0) return HHR_ERR_INVALID_ARG;
+  PageAttnArgs a{};
+  // The list kernels only read the cache.
+  a.q = q; a.k = const_cast<void*>(k_cache); a.v = const_cast<void*>(v_cache);
+  a.k_exp = const_cast<uint8_t*>(k_exp); a.v_exp = const_cast<uint8_t*>(v_exp);
+  a.page_table = page_table; a.seq_len = seq_len; a.q_pos = q_pos; a.blocks = blocks;
+  a.block_count = block_count; a.out = out; a.out_bf16 = out_bf16; a.lse = lse;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.T = n_queries; a.m_max = m_max;
+  return launch_page_attn<true>(d, a, k_exp != nullptr, units, workspace, (cudaStream_t)stream);
 }
 
 // ---------------------------------------------------------------------------

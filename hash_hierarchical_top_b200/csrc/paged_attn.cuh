@@ -1,0 +1,599 @@
+// Attention of one query token over whole pages of the cache: every page of a sequence (dense
+// decode), or the pages of a per-query list (block-sparse decode and query chunks), from a bf16
+// or an 8-bit cache.
+//
+// Row = one (sequence, query token, selection row): gs query heads that share the K/V rows of
+// one KV head. o_h = sum_j w_hj v_j / sum_j w_hj with w_hj = exp(scale q_h . k_j - max), in one
+// pass: every warp keeps a running maximum, sum and output per head (fp32) over its own keys and
+// rescales them when the maximum grows; the warps of a CTA are joined in shared memory, the CTAs
+// of a row by page_join_kernel.
+//
+// What bounds it: the K/V bytes (512 B per key and KV head in bf16, 258 B in 8 bits) against 4
+// flops per byte and head, far below the tensor cores' balance. So the design keeps loads in
+// flight and spends few instructions per byte:
+//   - K and V go from global memory straight into registers as 16-byte loads in the layout that
+//     the matrix instructions want, with no pass through shared memory and no barrier in the
+//     loop: 16 warps of 8 KB each keep 128 KB in flight per SM. The order of the channels in a
+//     dot product is free, so lane (g, t) = (lane / 4, lane % 4) of S = Q K^T loads whole 16-byte
+//     pieces t, t + 4, ... of key g and the query fragments follow that order; in O^T = V^T P^T
+//     the channels are the rows of A, so a lane that holds 16-byte pieces of the keys 2t, 2t + 1,
+//     2t + 8, 2t + 9 only interleaves key pairs (one byte permute per register).
+//   - S has the heads on M (rows >= gs are zero) and the keys on N, so its accumulator is
+//     directly the B operand of O^T, whose N = 8 columns are the heads: nothing is exchanged
+//     between lanes but the maxima.
+//   - Page ids are loaded two steps ahead of the rows they locate, the rows one step ahead of
+//     their use.
+// P is used as two parts (hi + lo): bf16 parts leave 2^-17 of it, f16 parts 2^-22, so that the
+// fp32 output is not limited by the matrix operands' type.
+//
+// 8-bit cache: e4m3 numbers become f16 exactly. Q is scaled by a power of two per head so that
+// its largest channel is in [2^14, 2^15): bf16 queries are then exact in f16 down to 2^-38 of
+// the largest channel (smaller ones round to 0). The key's exponent multiplies its logit; the
+// value's exponent goes into the weight, relative to the warp's running largest one (E_run), and
+// 2^14 more keeps small weights out of f16's subnormal range.
+//
+// Split of the work: the rows' keys, in units of kUnitKeys, are laid end to end and divided
+// evenly over the CTAs (two per SM), whatever the lengths; a CTA's share covers the end of one
+// row, whole rows, the beginning of another. Whole rows are written directly; a share that
+// covers part of a row writes a partial (at most two per CTA), joined by page_join_kernel.
+#pragma once
+#include "attn.cuh"
+#include "common.cuh"
+#include "kv8.cuh"
+
+namespace hhr {
+
+constexpr int kPaWarps = 8;
+constexpr int kPaThreads = kPaWarps * 32;
+constexpr int kPaCtasPerSm = 2;
+constexpr int kUnitKeys = 128;
+
+struct PageAttnArgs {
+  const uint16_t* q;      // [B][T][Hq][d]
+  const uint16_t* k_new;  // dense: newest rows [B][G][d], appended before they are read; or null
+  const uint16_t* v_new;
+  void* k;                // [n_phys][G][P][d] bf16 or e4m3
+  void* v;
+  uint8_t* k_exp;         // 8-bit cache: [n_phys][G][P]
+  uint8_t* v_exp;
+  const int32_t* page_table;
+  const int32_t* seq_len;
+  const int32_t* q_pos;        // [B][T] or null
+  const int32_t* blocks;       // list: [B][T][Gs][m_max]
+  const int32_t* block_count;  // list: [B][T][Gs]
+  float* part_o;               // [2 CTAs][gs][d]
+  float* part_ml;              // [2 CTAs][gs][2]
+  void* out;                   // [B][T][Hq][d] f32 or bf16
+  float* lse;                  // [B][T][Hq] or null
+  float scale_log2;
+  int out_bf16;
+  int B, T, Hq, G, Gs, kv_div, P, maxp, n_phys, m_max;
+  uint32_t p_mul;              // ceil(2^32 / P): j / P = umulhi(j, p_mul) for P > 1
+  int n_ctas;
+};
+
+// j / P for 0 <= j < 2^24, P <= 256: the error of j p_mul / 2^32 is below j P / 2^32 < 1 / P.
+__device__ __forceinline__ int page_of(const PageAttnArgs& a, int j) {
+  return a.P == 1 ? j : (int)__umulhi((uint32_t)j, a.p_mul);
+}
+
+// Keys of a dense row, and units of a row (at least one, so that an empty row is written).
+__device__ __forceinline__ int dense_len(const PageAttnArgs& a, int b) {
+  return min(max(a.seq_len[b], 0), a.maxp * a.P);
+}
+__device__ __forceinline__ int units_of(int keys) {
+  return max(1, (keys + kUnitKeys - 1) / kUnitKeys);
+}
+
+// CTA c's share of `total` units over n CTAs: [c total / n, (c + 1) total / n). n <= total.
+__device__ __forceinline__ int share_begin(int c, int total, int n) {
+  return (int)((long long)c * total / n);
+}
+// The CTA whose share holds unit u.
+__device__ __forceinline__ int share_of(int u, int total, int n) {
+  return (int)((((long long)u + 1) * n - 1) / total);
+}
+
+// Block-wide (256 threads): the sum of units over sequences [0, B) of dense rows, each counted
+// Gs times, and either the place of unit `find` (find >= 0: *at_b, the sequence, *at_u the units
+// before it inside that sequence) or the units before sequence -1 - find (*at_u). sh: 40 ints.
+__device__ __forceinline__ int dense_scan(const PageAttnArgs& a, int find, int* sh, int* at_b,
+                                          int* at_u) {
+  const int tid = threadIdx.x, per = (a.B + blockDim.x - 1) / blockDim.x;
+  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) sum += units_of(dense_len(a, b)) * a.Gs;
+  int total;
+  int before = block_excl_scan<true>(sum, sh, &total);
+  if (find >= 0) {
+    if (find >= before && find < before + sum) {
+      int b = b0;
+      for (; b < b1 - 1; ++b) {
+        const int u = units_of(dense_len(a, b)) * a.Gs;
+        if (find < before + u) break;
+        before += u;
+      }
+      sh[36] = b;
+      sh[37] = find - before;
+    }
+  } else {
+    const int want = -1 - find;
+    if (want >= b0 && want < b1) {
+      for (int b = b0; b < want; ++b) before += units_of(dense_len(a, b)) * a.Gs;
+      sh[36] = want;
+      sh[37] = before;
+    }
+  }
+  __syncthreads();
+  *at_b = sh[36];
+  *at_u = sh[37];
+  return total;
+}
+
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// f16 counterpart of mma_16816, and the f16 packing of two floats.
+__device__ __forceinline__ void mma_16816_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                              uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float x, float y) {
+  const __half2 h = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two weights as hi + lo parts of the matrix operand's type.
+template <bool K8>
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
+  if constexpr (K8) {
+    hi = pack_f16(x, y);
+    const float2 h = f16x2_to_f2(hi);
+    lo = pack_f16(x - h.x, y - h.y);
+  } else {
+    hi = pack_bf16(x, y);
+    lo = pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
+  }
+}
+
+// Where the keys of one row lie.
+struct RowKeys {
+  const int32_t* pages;   // the sequence's page-table row
+  const int32_t* blocks;  // list: the row's blocks
+  int n;                  // key slots: dense, the length; list, listed blocks * P
+  int limit;              // keys at positions >= limit are not attended to
+  uint32_t g;             // KV head
+};
+
+// The page id that slot j needs (list: through the block list), or a negative number with the
+// status word set; -1 alone when the slot holds no key.
+template <bool kList>
+__device__ __forceinline__ int block_of(const PageAttnArgs& a, const RowKeys& r, int j) {
+  if (j >= r.n) return -1;
+  if (!kList) return page_of(a, j);
+  const int p = r.blocks[page_of(a, j)];
+  if (p < 0 || p >= a.maxp) {
+    flag_status(kStatusBadToken);
+    return -1;
+  }
+  return p;
+}
+__device__ __forceinline__ int phys_of(const PageAttnArgs& a, const RowKeys& r, int block) {
+  if (block < 0 || block * a.P >= r.limit) return -1;
+  const int phys = r.pages[block];
+  if (phys < 0 || phys >= a.n_phys) {
+    flag_status(kStatusBadPage);
+    return -1;
+  }
+  return phys;
+}
+__device__ __forceinline__ uint32_t row_of(const PageAttnArgs& a, const RowKeys& r, int j,
+                                           int block, int phys) {
+  const int slot = j - page_of(a, j) * a.P;
+  if (phys < 0 || block * a.P + slot >= r.limit) return kNoRow;
+  return ((uint32_t)phys * (uint32_t)a.G + r.g) * (uint32_t)a.P + (uint32_t)slot;
+}
+
+// Keys [k0, k1) of a row, over the CTA's warps: the state of every head is left in shared
+// memory (mo [warps][8][d], ml [warps][8][2]).
+template <bool K8, bool kList>
+__device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKeys& rk,
+                                             const uint16_t* q, int gs, int k0, int k1, float* mo,
+                                             float* ml) {
+  constexpr int S = K8 ? 32 : 16;   // keys of a warp's step
+  constexpr int NT = S / 8;         // 8-key tiles of S
+  constexpr int RB = K8 ? kD : 2 * kD;  // bytes of a cache row
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int gq = lane >> 2, tq = lane & 3;
+  const char* kb = reinterpret_cast<const char*>(a.k);
+  const char* vb = reinterpret_cast<const char*>(a.v);
+
+  // Query fragments: MMA (c, s) takes the channels [ch, ch + 4) of lane tq, ch = (16 or 8)
+  // (tq + 4c) + 4s, as k = 2tq, 2tq + 1, 2tq + 8, 2tq + 9.
+  uint32_t qa[8][2];
+  float hs = a.scale_log2;
+  {
+    const bool hv = gq < gs;
+    const uint2* q4 = reinterpret_cast<const uint2*>(q + (size_t)(hv ? gq : 0) * kD);
+    uint2 w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int ch = K8 ? 16 * (tq + 4 * (i >> 2)) + 4 * (i & 3) : 8 * (tq + 4 * (i >> 1)) + 4 * (i & 1);
+      w[i] = hv ? q4[ch >> 2] : make_uint2(0u, 0u);
+    }
+    if constexpr (K8) {
+      uint32_t top = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        top = max(max(top, max(w[i].x & 0x7fffu, (w[i].x >> 16) & 0x7fffu)),
+                  max(w[i].y & 0x7fffu, (w[i].y >> 16) & 0x7fffu));
+      top = max(top, __shfl_xor_sync(kFull, top, 1));
+      top = max(top, __shfl_xor_sync(kFull, top, 2));
+      const uint32_t E = max(top >> 7, 15u);          // exponent field of the largest channel
+      const float up = __uint_as_float((268u - E) << 23);  // 2^(14 - (E - 127))
+      hs = a.scale_log2 * __uint_as_float((E - 14u) << 23);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        qa[i][0] = pack_f16(bf16_lo(w[i].x) * up, bf16_hi(w[i].x) * up);
+        qa[i][1] = pack_f16(bf16_lo(w[i].y) * up, bf16_hi(w[i].y) * up);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        qa[i][0] = w[i].x;
+        qa[i][1] = w[i].y;
+      }
+    }
+  }
+
+  float m_run = -INFINITY, l_run = 0.f;  // head gq (m_run the same on its 4 lanes)
+  uint32_t e_run = 0u;                   // 8-bit: largest exponent byte of a value so far
+  float oacc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.f;
+
+  uint4 kf[8], vf[8];
+  uint32_t ex = 0u;  // 8-bit: exponent bytes of this lane's key (K low, V next)
+  const int base = k0 + warp * S, stride = kPaWarps * S;
+  const int lk = K8 ? lane : (lane & 15);  // the key of a step that this lane locates
+
+  auto load_k = [&](uint32_t row) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const uint32_t o = __shfl_sync(kFull, row, 8 * j + gq);
+      const char* p = kb + (size_t)o * RB + 16 * tq;
+#pragma unroll
+      for (int c = 0; c < 8 / NT; ++c)
+        kf[j * (8 / NT) + c] = o != kNoRow ? ldg_stream(p + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if constexpr (K8) ex = row != kNoRow ? (uint32_t)a.k_exp[row] | (uint32_t)a.v_exp[row] << 8 : 0u;
+  };
+  // vf: bf16: [key of 2t, 2t+1, 2t+8, 2t+9][piece gq, gq + 8]; 8-bit: [16-key group][key], piece gq.
+  auto load_v = [&](uint32_t row) {
+#pragma unroll
+    for (int i = 0; i < S / 4; ++i) {
+      const int key = 16 * (i >> 2) + 8 * ((i >> 1) & 1) + (i & 1) + 2 * tq;
+      const uint32_t o = __shfl_sync(kFull, row, key);
+      const char* p = vb + (size_t)o * RB + 16 * gq;
+      if constexpr (K8) {
+        vf[i] = o != kNoRow ? ldg_stream(p) : make_uint4(0u, 0u, 0u, 0u);
+      } else {
+        vf[2 * i] = o != kNoRow ? ldg_stream(p) : make_uint4(0u, 0u, 0u, 0u);
+        vf[2 * i + 1] = o != kNoRow ? ldg_stream(p + 128) : make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+  };
+  auto block_at = [&](int j) { return j < k1 ? block_of<kList>(a, rk, j) : -1; };
+
+  int j0 = base + lk;
+  int blk = block_at(j0);
+  uint32_t row = row_of(a, rk, j0, blk, phys_of(a, rk, blk));
+  int blk1 = block_at(j0 + stride);
+  int phys1 = phys_of(a, rk, blk1);
+  int blk2 = block_at(j0 + 2 * stride);
+  load_k(row);
+  load_v(row);
+  uint32_t ex_cur = ex;
+  for (int s0 = base; s0 < k1; s0 += stride, j0 += stride) {
+    // The next step's rows, and the page ids of the one after.
+    const uint32_t row_next = row_of(a, rk, j0 + stride, blk1, phys1);
+    blk1 = blk2;
+    phys1 = phys_of(a, rk, blk1);
+    blk2 = block_at(j0 + 3 * stride);
+    const bool more = s0 + stride < k1;
+
+    float sacc[NT][4];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      sacc[j][0] = sacc[j][1] = sacc[j][2] = sacc[j][3] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (K8) {
+          const uint32_t w = word_of(kf[2 * j + (i >> 2)], i & 3);
+          mma_16816_f16(sacc[j], qa[i][0], 0u, qa[i][1], 0u, e4m3x2_to_f16x2(w & 0xffffu),
+                        e4m3x2_to_f16x2(w >> 16));
+        } else {
+          const uint4& w = kf[4 * j + (i >> 1)];
+          mma_16816(sacc[j], qa[i][0], 0u, qa[i][1], 0u, word_of(w, 2 * (i & 1)),
+                    word_of(w, 2 * (i & 1) + 1));
+        }
+      }
+    }
+    const unsigned ok = __ballot_sync(kFull, row != kNoRow);
+    ex_cur = ex;
+    if (more) load_k(row_next);
+
+    // Logits in log2 units, of head gq and the keys 8j + 2tq, 8j + 2tq + 1.
+    float mx = -INFINITY;
+    uint32_t e2[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int key = 8 * j + 2 * tq + i;
+        float sc = hs;
+        if constexpr (K8) {
+          e2[j][i] = __shfl_sync(kFull, ex_cur, key);
+          sc *= exp_scale(e2[j][i] & 0xffu);
+        }
+        sacc[j][i] = (ok >> key & 1u) ? sacc[j][i] * sc : -INFINITY;
+        mx = fmaxf(mx, sacc[j][i]);
+      }
+    }
+    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+    const float m_new = fmaxf(m_run, mx);
+    uint32_t e_new = e_run;
+    if constexpr (K8) e_new = max(e_run, __reduce_max_sync(kFull, ex_cur >> 8));
+    if (__any_sync(kFull, m_new > m_run) || e_new != e_run) {
+      const float c = m_new > m_run ? exp2f(m_run - m_new) : 1.f;
+      l_run *= c;
+      float ca = __shfl_sync(kFull, c, 8 * tq), cb = __shfl_sync(kFull, c, 8 * tq + 4);
+      if constexpr (K8) {
+        const float ec = exp_scale((uint32_t)max(127 + (int)e_run - (int)e_new, 0));
+        ca *= ec;
+        cb *= ec;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        oacc[i][0] *= ca; oacc[i][2] *= ca;
+        oacc[i][1] *= cb; oacc[i][3] *= cb;
+      }
+      m_run = m_new;
+      e_run = e_new;
+    }
+    const float mu = m_run == -INFINITY ? 0.f : m_run;
+    uint32_t ph[NT], pl[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      float p[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        p[i] = exp2f(sacc[j][i] - mu);
+        l_run += p[i];
+        if constexpr (K8)
+          p[i] *= exp_scale((uint32_t)max(127 + 14 + (int)(e2[j][i] >> 8) - (int)e_run, 0));
+      }
+      split_pair<K8>(p[0], p[1], ph[j], pl[j]);
+    }
+    // O^T += V^T P^T, 16 keys at a time.
+#pragma unroll
+    for (int h = 0; h < S / 16; ++h) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint32_t a0, a1, a2, a3;
+        if constexpr (K8) {
+          const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+          const uint32_t x = __byte_perm(word_of(vf[4 * h], i >> 1), word_of(vf[4 * h + 1], i >> 1), sel);
+          const uint32_t y = __byte_perm(word_of(vf[4 * h + 2], i >> 1), word_of(vf[4 * h + 3], i >> 1), sel);
+          a0 = e4m3x2_to_f16x2(x & 0xffffu);
+          a1 = e4m3x2_to_f16x2(x >> 16);
+          a2 = e4m3x2_to_f16x2(y & 0xffffu);
+          a3 = e4m3x2_to_f16x2(y >> 16);
+          mma_16816_f16(oacc[i], a0, a1, a2, a3, ph[2 * h], ph[2 * h + 1]);
+          mma_16816_f16(oacc[i], a0, a1, a2, a3, pl[2 * h], pl[2 * h + 1]);
+        } else {
+          const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u;
+          a0 = __byte_perm(word_of(vf[0], i >> 1), word_of(vf[2], i >> 1), sel);
+          a1 = __byte_perm(word_of(vf[1], i >> 1), word_of(vf[3], i >> 1), sel);
+          a2 = __byte_perm(word_of(vf[4], i >> 1), word_of(vf[6], i >> 1), sel);
+          a3 = __byte_perm(word_of(vf[5], i >> 1), word_of(vf[7], i >> 1), sel);
+          mma_16816(oacc[i], a0, a1, a2, a3, ph[0], ph[1]);
+          mma_16816(oacc[i], a0, a1, a2, a3, pl[0], pl[1]);
+        }
+      }
+    }
+    if (more) load_v(row_next);
+    row = row_next;
+  }
+
+  l_run += __shfl_xor_sync(kFull, l_run, 1);
+  l_run += __shfl_xor_sync(kFull, l_run, 2);
+  // oacc[i]: channel c0 (elements 0, 1) and c1 (2, 3) of the heads 2tq, 2tq + 1.
+  // 8-bit: 2^-14 and the running exponent, one after the other (2^(e_run - 141) may be subnormal).
+  const float os = K8 ? 6.103515625e-05f : 1.f, oe = K8 ? exp_scale(e_run) : 1.f;
+  float* mw = mo + (size_t)warp * kMaxGroup * kD;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int c0 = K8 ? 16 * gq + 2 * i : 8 * gq + i, c1 = K8 ? c0 + 1 : c0 + 64;
+    mw[(2 * tq) * kD + c0] = oacc[i][0] * os * oe;
+    mw[(2 * tq + 1) * kD + c0] = oacc[i][1] * os * oe;
+    mw[(2 * tq) * kD + c1] = oacc[i][2] * os * oe;
+    mw[(2 * tq + 1) * kD + c1] = oacc[i][3] * os * oe;
+  }
+  if (tq == 0) {
+    ml[(warp * kMaxGroup + gq) * 2] = m_run;
+    ml[(warp * kMaxGroup + gq) * 2 + 1] = l_run;
+  }
+}
+
+// Writes output channel c of query head `head` (and, for c == 0, its log of the weights' sum).
+__device__ __forceinline__ void put_out(const PageAttnArgs& a, size_t head, int c, float M, float L,
+                                        float O) {
+  const float o = L == 0.f ? 0.f : O / L;
+  if (a.out_bf16)
+    reinterpret_cast<__nv_bfloat16*>(a.out)[head * kD + c] = __float2bfloat16_rn(o);
+  else
+    reinterpret_cast<float*>(a.out)[head * kD + c] = o;
+  if (c == 0 && a.lse != nullptr)
+    a.lse[head] = ((M == -INFINITY ? 0.f : M) + log2f(L)) * 0.6931471805599453f;
+}
+
+inline size_t page_attn_smem() { return (size_t)kPaWarps * kMaxGroup * (kD + 2) * 4; }
+
+template <bool K8, bool kList>
+__global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(PageAttnArgs a) {
+  extern __shared__ float4 pa_smem[];
+  __shared__ int sh[40];
+  float* mo = reinterpret_cast<float*>(pa_smem);
+  float* ml = mo + kPaWarps * kMaxGroup * kD;
+  const int tid = threadIdx.x, gs = a.Hq / a.Gs;
+  int total, b, off, c = blockIdx.x, n = a.n_ctas;
+  if (kList) {
+    total = a.B * a.T * a.Gs * units_of(a.m_max * a.P);
+  } else {
+    total = dense_scan(a, -1, sh, &b, &off);
+  }
+  n = min(n, total);
+  if (c >= n) return;
+  int u = share_begin(c, total, n);
+  const int end = share_begin(c + 1, total, n);
+  if (!kList) dense_scan(a, u, sh, &b, &off);
+  int row = 0, ub;  // selection row (over all sequences and tokens), units of it
+  if (kList) {
+    ub = units_of(a.m_max * a.P);
+    row = u / ub;
+    off = u - row * ub;
+  } else {
+    ub = units_of(dense_len(a, b));
+    row = b * a.Gs + off / ub;
+    off %= ub;
+  }
+  while (true) {
+    const int take = min(end - u, ub - off);
+    const int bt = row / a.Gs, r = row - bt * a.Gs;
+    if (kList) b = bt / a.T;
+    RowKeys rk;
+    rk.pages = a.page_table + (size_t)b * a.maxp;
+    rk.g = (uint32_t)(a.kv_div == 1 ? r : r / a.kv_div);
+    rk.limit = dense_len(a, b);
+    if (a.q_pos != nullptr) rk.limit = min(rk.limit - 1, a.q_pos[bt]) + 1;
+    rk.blocks = kList ? a.blocks + (size_t)row * a.m_max : nullptr;
+    rk.n = kList ? min(max(a.block_count[row], 0), a.m_max) * a.P : rk.limit;
+    if (!kList && tid == 0 && a.seq_len[b] > a.maxp * a.P) flag_status(kStatusBadToken);
+    if (!kList && a.k_new != nullptr && off + take == ub && rk.n > 0) {
+      // The newest row lies in this segment: it is written before any of it is read.
+      const int t = rk.n - 1, lp = page_of(a, t);
+      const int phys = phys_of(a, rk, lp);
+      if (tid < 32 && phys >= 0) {
+        const int l16 = tid & 15;
+        const uint32_t o = row_of(a, rk, t, lp, phys);
+        const uint16_t* src = (tid < 16 ? a.k_new : a.v_new) + ((size_t)b * a.G + rk.g) * kD;
+        char* dst = reinterpret_cast<char*>(tid < 16 ? a.k : a.v);
+        const uint4 w = reinterpret_cast<const uint4*>(src)[l16];
+        if constexpr (K8) {
+          const uint32_t x = row_exponent(row_top16(w, 0xffffu << (tid & 16)));
+          *reinterpret_cast<uint2*>(dst + (size_t)o * kD + 8 * l16) = quantise8(w, x);
+          if (l16 == 0) (tid < 16 ? a.k_exp : a.v_exp)[o] = (uint8_t)x;
+        } else {
+          *reinterpret_cast<uint4*>(dst + (size_t)o * 2 * kD + 16 * l16) = w;
+        }
+      }
+    }
+    __syncthreads();  // the new row is visible; the previous segment's state has been read
+    const size_t head0 = (size_t)bt * a.Hq + (size_t)r * gs;
+    page_segment<K8, kList>(a, rk, a.q + head0 * kD, gs, off * kUnitKeys,
+                            min(rk.n, (off + take) * kUnitKeys), mo, ml);
+    __syncthreads();
+    const bool whole = off == 0 && take == ub;
+    const size_t slot = 2 * (size_t)c + (off == 0 ? 1 : 0);
+    for (int i = tid; i < gs * kD; i += kPaThreads) {
+      const int h = i / kD, ch = i % kD;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kPaWarps; ++w) M = fmaxf(M, ml[(w * kMaxGroup + h) * 2]);
+      const float mu = M == -INFINITY ? 0.f : M;
+      float L = 0.f, O = 0.f;
+#pragma unroll
+      for (int w = 0; w < kPaWarps; ++w) {
+        const float f = exp2f(ml[(w * kMaxGroup + h) * 2] - mu);
+        L = fmaf(f, ml[(w * kMaxGroup + h) * 2 + 1], L);
+        O = fmaf(f, mo[((size_t)w * kMaxGroup + h) * kD + ch], O);
+      }
+      if (whole) {
+        put_out(a, head0 + h, ch, M, L, O);
+      } else {
+        a.part_o[(slot * gs + h) * kD + ch] = O;
+        if (ch == 0) {
+          a.part_ml[(slot * gs + h) * 2] = M;
+          a.part_ml[(slot * gs + h) * 2 + 1] = L;
+        }
+      }
+    }
+    u += take;
+    if (u >= end) break;
+    ++row;
+    off = 0;
+    if (!kList) {
+      b = row / a.Gs;
+      ub = units_of(dense_len(a, b));
+    }
+  }
+  pdl_trigger();
+}
+
+// Joins the partials of one row: the CTAs c0..c1 whose shares touch it, the first of them with
+// its "row begins here" slot, the others with their "row goes on" slot. One CTA per row; rows
+// that one CTA covered are already written.
+constexpr int kJoinThreads = 256;
+template <bool kList>
+__global__ void __launch_bounds__(kJoinThreads) page_join_kernel(PageAttnArgs a) {
+  __shared__ int sh[40];
+  const int row = blockIdx.x, tid = threadIdx.x, gs = a.Hq / a.Gs;
+  int total, first, ub, b, off;
+  if (kList) {
+    ub = units_of(a.m_max * a.P);
+    total = a.B * a.T * a.Gs * ub;
+    first = row * ub;
+  } else {
+    const int bs = row / a.Gs;
+    total = dense_scan(a, -1 - bs, sh, &b, &off);
+    ub = units_of(dense_len(a, bs));
+    first = off + (row - bs * a.Gs) * ub;
+  }
+  const int n = min(a.n_ctas, total);
+  const int c0 = share_of(first, total, n), c1 = share_of(first + ub - 1, total, n);
+  pdl_wait();
+  if (c0 == c1) return;
+  const int bt = row / a.Gs, r = row - bt * a.Gs;
+  const size_t head0 = (size_t)bt * a.Hq + (size_t)r * gs;
+  for (int i = tid; i < gs * kD; i += kJoinThreads) {
+    const int h = i / kD, ch = i % kD;
+    auto slot = [&](int c) { return ((size_t)2 * c + (c == c0 ? 1 : 0)) * gs + h; };
+    float M = -INFINITY;
+    for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(a.part_ml + slot(c) * 2));
+    const float mu = M == -INFINITY ? 0.f : M;
+    float L = 0.f, O = 0.f;
+    for (int c = c0; c <= c1; ++c) {
+      const float f = exp2f(__ldcg(a.part_ml + slot(c) * 2) - mu);
+      L = fmaf(f, __ldcg(a.part_ml + slot(c) * 2 + 1), L);
+      O = fmaf(f, __ldcg(a.part_o + slot(c) * kD + ch), O);
+    }
+    put_out(a, head0 + h, ch, M, L, O);
+  }
+}
+
+}  // namespace hhr

@@ -801,16 +801,18 @@ __device__ __forceinline__ SelCut block_select_cut(const float* sc, int n, uint3
 // Block-wide selection (NT threads, call uniformly): the k largest finite scores of sc[0..n),
 // ties to the lower index, written in ascending index order to out[0..k) (global or shared
 // memory); see block_select_cut for k. unit > 0 maps index i to kept_units[i / unit] * unit
-// + i % unit. keys: shared scratch of n words (16-byte aligned). Returns k.
+// + i % unit. sink, local: forced entries (block_select_cut). keys: shared scratch of n words
+// (16-byte aligned). Returns k.
 template <int NT = kSelThreads, int LU = kSelLoadUnroll, int HC = 1>
 __device__ __forceinline__ int block_select_largest(const float* sc, int n, uint32_t* keys,
                                                     SelShared<HC>& sh, bool by_kept,
                                                     int m_pages, int keep_div, int top_k,
                                                     int32_t* out, int out_stride,
-                                                    const int32_t* kept_units, int unit) {
+                                                    const int32_t* kept_units, int unit,
+                                                    int sink = 0, int local = 0) {
   const int tid = threadIdx.x;
-  const SelCut c =
-      block_select_cut<NT, LU, HC>(sc, n, keys, sh, by_kept, m_pages, keep_div, top_k);
+  const SelCut c = block_select_cut<NT, LU, HC>(sc, n, keys, sh, by_kept, m_pages, keep_div,
+                                                top_k, sink, local);
   // Compaction in index order over contiguous per-thread ranges. Before thread t's range
   // are gt_before keys above the cut and eq_before equal to it, of which the first
   // min(eq_before, rem) are taken.

@@ -291,12 +291,118 @@ int hhr_sparse_attn_noalloc(const hhr_dims* dims, const uint16_t* q, const uint1
                             const int32_t* seq_len, const int32_t* idx, const int32_t* count,
                             int top_k, float scale, float* out, void* stream);
 
+/* ---- The 8-bit K/V cache ---------------------------------------------------------------
+ * Half the bytes of the bf16 cache, for hhr_paged_attn and hhr_block_attn. Layouts:
+ *   k, v         : e4m3 (uint8 bit patterns) [n_phys_pages][G][P][d]
+ *   k_exp, v_exp : uint8 [n_phys_pages][G][P], one exponent byte per key row and KV head
+ * A row stands for e4m3 * 2^(byte - 127). Quantising a row x takes the smallest whole e of
+ * [-117, 119] with max|x| <= 448 * 2^e (-117 for zeros), divides by 2^e (exactly) and rounds
+ * each channel once, to the nearest e4m3 number, ties to even: half a step is 2^-4 of the
+ * channel, and never more than 2^(e - 10) where that is larger. A NaN stays a NaN and does not
+ * count in max|x|; a row with an infinity takes e = 119 and holds it as +-448 * 2^119. */
+
+/* Writes new key and value rows into an 8-bit cache.
+ *   k_new, v_new : bf16; row (b, i, g) starts at ((b * max_new + i) * token_stride + g * d)
+ *                  elements: [B][max_new][G][d] when token_stride = G * d, or a slice of a
+ *                  wider product (a fused Q|K|V row) otherwise
+ *   token_stride : elements, >= G * d, a multiple of 8
+ *   start, n_new, max_new : as in hhr_encode_keys; rows [0, n_new[b]) of sequence b go to the
+ *                  logical positions [start[b], start[b] + n_new[b]). The other rows of
+ *                  k_new, v_new are not read, no other row of the cache is written.
+ *   block_mean   : NULL, or f32 [n_phys_pages][G][d]: the mean of every valid key of each
+ *                  touched page (positions < start[b] + n_new[b]), as the 8-bit cache holds
+ *                  them: what hhr_block_select scores.
+ * A page-table entry out of range skips that page and is flagged. */
+int hhr_append_kv8(const hhr_dims* dims, const uint16_t* k_new, const uint16_t* v_new,
+                   int64_t token_stride, const int32_t* start, const int32_t* n_new, int max_new,
+                   const int32_t* page_table, uint8_t* k, uint8_t* v, uint8_t* k_exp,
+                   uint8_t* v_exp, float* block_mean, void* stream);
+
+/* Reads an 8-bit cache back: the rows at the logical positions [start[b], start[b] + n[b]) of
+ * each sequence as bf16 (exactly what the cache stands for), into
+ *   k_out, v_out : bf16 [B][max_n][G][d]
+ * Rows past n[b] are left as they were, and so are rows whose page is out of range (flagged).
+ * n[b] > max_n is clipped and flagged. */
+int hhr_read_kv8(const hhr_dims* dims, const uint8_t* k, const uint8_t* v, const uint8_t* k_exp,
+                 const uint8_t* v_exp, const int32_t* page_table, const int32_t* start,
+                 const int32_t* n, int max_n, uint16_t* k_out, uint16_t* v_out, void* stream);
+
+/* ---- Attention over whole pages ---------------------------------------------------------
+ * Two calls that attend to every key of the pages they are given, from a bf16 cache (k_exp and
+ * v_exp NULL) or an 8-bit one. out[..][h] = sum_j softmax_j(scale * q_h . k_j) v_j, with
+ * statistics and sums in fp32; a row with no key gives zeros. Keys outside the mask are never
+ * read into the sums, whatever the cache holds there.
+ *   out      : [B][T][Hq][d], f32, or bf16 with out_bf16 = 1 (rounded once)
+ *   lse      : NULL, or f32 [B][T][Hq]: log sum_j exp(scale * q_h . k_j), with which outputs
+ *              over disjoint key sets can be joined; -inf for a row with no key
+ *   workspace: at least the call's *_workspace_bytes (0 on invalid input), on the device that
+ *              the call runs on. Its contents need not be kept or cleared, but calls that can
+ *              overlap on the GPU need one each.
+ * The keys of all rows are divided evenly over the GPU, whatever the sequences' lengths; rows
+ * that are split are joined in a fixed order, so that equal inputs give equal bits. */
+
+size_t hhr_paged_attn_workspace_bytes(const hhr_dims* dims);
+
+/* Dense attention of one new token per sequence (T = 1) over positions [0, seq_len[b]): the
+ * step that hhr_decode_step shortens, for short sequences and for layers kept dense.
+ *   q            : bf16 [B][Hq][d]
+ *   k_new, v_new : NULL, or bf16 [B][G][d]: the rows of position seq_len[b] - 1, written into
+ *                  the cache (quantised as hhr_append_kv8 does, when it holds 8 bits) by this
+ *                  call before they are attended to. A sequence of length 0 writes nothing.
+ *   dims.select_per_head must be 0. seq_len[b] beyond max_pages_per_seq * P is clipped to it
+ *   and flagged; a key whose page-table entry is out of range is skipped and flagged. */
+int hhr_paged_attn(const hhr_dims* dims, const uint16_t* q, const uint16_t* k_new,
+                   const uint16_t* v_new, void* k_cache, void* v_cache, uint8_t* k_exp,
+                   uint8_t* v_exp, const int32_t* page_table, const int32_t* seq_len, float scale,
+                   void* out, int out_bf16, float* lse, void* workspace, size_t ws_bytes,
+                   void* stream);
+
+size_t hhr_block_select_workspace_bytes(const hhr_dims* dims, int n_queries);
+
+/* Block selection for a chunk of n_queries = T query tokens per sequence (HISA page, Abstract:
+ * a block-level coarse filter over pooled block representatives; here per KV group of a
+ * grouped-query model, page = block). Row (b, t, g), eligible blocks p < n,
+ * n = ceil(min(seq_len[b], q_pos[b][t] + 1) / P):
+ *   score_p = (sum_{h in g} q_h) . block_mean_p, the 64-bit sum rounded to f32 once;
+ * keeps the min(m_pages, n) blocks of largest score, ties to the lower block. A block whose
+ * score is -inf or NaN is not kept. Forced sink and local pages (opts, as in hhr_select; the
+ * local ones are the last of the query's n) are kept whatever their score.
+ *   q          : bf16 [B][T][Hq][d]
+ *   q_pos      : int32 [B][T], or NULL: every query sees the whole sequence
+ *   out_blocks : int32 [B][T][rows][m_max] ascending logical blocks, -1 past the count;
+ *                m_max = hhr_kept_max(dims, m_pages, 0)
+ *   out_count  : int32 [B][T][rows]
+ * rows = G, or Hq with dims.select_per_head ("sum" is then the row's own head). */
+int hhr_block_select(const hhr_dims* dims, int n_queries, const uint16_t* q,
+                     const int32_t* seq_len, const int32_t* q_pos, const int32_t* page_table,
+                     const float* block_mean, int m_pages, const hhr_select_opts* opts,
+                     int32_t* out_blocks, int32_t* out_count, void* workspace, size_t ws_bytes,
+                     void* stream);
+
+size_t hhr_block_attn_workspace_bytes(const hhr_dims* dims, int n_queries, int m_max);
+
+/* Attention of each query of a chunk over its own blocks: row (b, t, r) attends to the keys of
+ * blocks[b][t][r][0..block_count) at positions < min(seq_len[b], q_pos[b][t] + 1).
+ *   q           : bf16 [B][T][Hq][d]
+ *   q_pos       : int32 [B][T], or NULL: no causal limit inside the sequence
+ *   blocks      : int32 [B][T][rows][m_max], logical blocks in any order (as hhr_block_select
+ *                 or hhr_select's trace->kept returns them); one listed twice counts twice; an
+ *                 entry outside [0, max_pages_per_seq) is skipped and flagged
+ *   block_count : int32 [B][T][rows], clipped to [0, m_max]
+ *   m_max       : row stride of blocks, 1..32768 */
+int hhr_block_attn(const hhr_dims* dims, int n_queries, const uint16_t* q, const void* k_cache,
+                   const void* v_cache, const uint8_t* k_exp, const uint8_t* v_exp,
+                   const int32_t* page_table, const int32_t* seq_len, const int32_t* q_pos,
+                   const int32_t* blocks, const int32_t* block_count, int m_max, float scale,
+                   void* out, int out_bf16, float* lse, void* workspace, size_t ws_bytes,
+                   void* stream);
+
 /* Kernels that hhr_profile_next can bracket with events. */
 typedef enum {
   HHR_KERNEL_ENCODE = 0,     /* hhr_encode_keys; hhr_decode_step's fused prologue */
   HHR_KERNEL_QPREP = 1,      /* hhr_select, hash mode, step a1 */
   HHR_KERNEL_BOUND = 2,      /* hhr_select, hash mode, step a2 bounds */
-  HHR_KERNEL_TOPM = 3,       /* hhr_select, indexer mode, top-m blocks */
+  HHR_KERNEL_TOPM = 3,       /* hhr_select, indexer mode, top-m blocks; hhr_block_select */
   HHR_KERNEL_HAMMING = 4,    /* hhr_select, hash mode, top-m pages + steps a3-a4 (fused) */
   HHR_KERNEL_BLOCK = 5,      /* hhr_select, indexer mode, block scores (or the whole
                                 selection, when it runs as one cluster per query) */
@@ -306,7 +412,12 @@ typedef enum {
   HHR_KERNEL_COMBINE = 9,    /* hhr_sparse_attn, merge of the chunks */
   HHR_KERNEL_ROW = 10,       /* hhr_decode_step, small batches: bounds, top-m, Hamming top-k
                                 and attention of each selection row in one cluster */
-  HHR_KERNEL_COUNT = 11
+  HHR_KERNEL_APPEND = 11,    /* hhr_append_kv8 */
+  HHR_KERNEL_READ = 12,      /* hhr_read_kv8 */
+  HHR_KERNEL_PAGE = 13,      /* hhr_paged_attn, hhr_block_attn: the keys */
+  HHR_KERNEL_JOIN = 14,      /* hhr_paged_attn, hhr_block_attn: join of split rows */
+  HHR_KERNEL_MEAN = 15,      /* hhr_block_select, block scores (its choice: HHR_KERNEL_TOPM) */
+  HHR_KERNEL_COUNT = 16
 } hhr_kernel;
 
 /* Measurement hook (no counterpart on the pages): the next launch of `kernel` by

@@ -1,0 +1,361 @@
+"""Dense paged attention and block-sparse attention on the GPU against float64 references, from
+bf16 and 8-bit caches whose unused slots hold NaNs."""
+import math
+
+import pytest
+import torch
+
+from hash_hierarchical_top_b200 import build, hhr
+from page_helpers import D, Paged, check_rows, quantise_ref, status_ok
+
+pytestmark = pytest.mark.gpu
+SCALE = 1.0 / math.sqrt(D)
+
+
+def dense(c, q, out_dtype=torch.float32, k_new=None, v_new=None, scale=SCALE, ws=None):
+    out = torch.full(q.shape, math.nan, dtype=out_dtype, device="cuda")
+    lse = torch.full(q.shape[:-1], math.nan, device="cuda")
+    if ws is None:
+        ws = torch.full((hhr.hhr_paged_attn_workspace_bytes(c.d),), 0xff, dtype=torch.uint8,
+                        device="cuda")
+    hhr.hhr_paged_attn(c.d, q, k_new, v_new, c.k, c.v, c.k_exp, c.v_exp, c.pt, c.seq_len, scale,
+                       out, ws, lse=lse)
+    return out, lse
+
+
+def check_dense(c, q, out, lse, scale=SCALE):
+    for b, n in enumerate(c.lens):
+        pos = torch.arange(n, device="cuda")
+        for g in range(c.G):
+            h = slice(g * c.gs, (g + 1) * c.gs)
+            check_rows(out[b, h], lse[b, h], q[b, h], c.rows("k", b, g, pos),
+                       c.rows("v", b, g, pos), scale, f"sequence {b}, KV head {g}")
+
+
+SHAPES = [  # lengths, KV heads, heads per KV head, page size
+    ([1], 1, 1, 1),
+    ([2, 1, 0, 3], 2, 8, 16),
+    ([517], 8, 4, 32),
+    ([127, 128, 129, 0, 255, 257], 3, 5, 32),
+    ([1000, 31], 1, 7, 17),
+    ([4096], 1, 1, 64),
+    ([5000, 1, 300], 2, 3, 5),
+    ([777, 2049], 4, 2, 256),
+    ([300], 2, 6, 1),
+    ([9001], 2, 8, 100),
+]
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("lens,G,gs,P", SHAPES)
+def test_dense(lens, G, gs, P, kv8, out_dtype):
+    build.build()
+    c = Paged(lens, G, gs, P, kv8, seed=len(lens) + P)
+    q = c.queries(len(lens))
+    out, lse = dense(c, q, out_dtype)
+    status_ok()
+    check_dense(c, q, out, lse)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_dense_many_ragged_sequences(kv8):
+    """More sequences than threads of a CTA, most of them short, one long."""
+    build.build()
+    lens = [(37 * i) % 90 for i in range(300)]
+    lens[211] = 20000
+    c = Paged(lens, 1, 4, 16, kv8, seed=8)
+    q = c.queries(300)
+    out, lse = dense(c, q)
+    status_ok()
+    check_dense(c, q, out, lse)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_dense_long_sequence_peaked_and_flat(kv8):
+    """64K keys split over every CTA: a query that one key dominates, and a nearly flat one whose
+    65536 weights are all of the same size."""
+    build.build()
+    n = 65536
+    c = Paged([n, n], 1, 2, 32, kv8, seed=3)
+    q = c.queries(2)
+    q[1] *= 0.01
+    k = c.rows("k", 0, 0, torch.arange(n, device="cuda"))
+    q[0, 0] = (k[54321] * 3).bfloat16()
+    out, lse = dense(c, q)
+    status_ok()
+    check_dense(c, q, out, lse)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_dense_large_and_small_magnitudes(kv8):
+    """Queries and keys far from 1, with one key or value row at another exponent than the rest."""
+    build.build()
+    for qs, ks in ((2.0 ** 40, 2.0 ** -42), (2.0 ** -60, 2.0 ** 58), (8.0, 4.0)):
+        c = Paged([600], 2, 4, 32, kv8, seed=11, scale=ks)
+        q = (c.queries(1).float() * qs).bfloat16()
+        if kv8:
+            phys = int(c.pt[0, 3])
+            c.v_exp[phys, :, 7] = 150            # 2^23 times the others' size
+            c.v_exp[phys, :, 8] = 60
+            c.k_exp[phys, :, 9] = 20
+        out, lse = dense(c, q)
+        status_ok()
+        check_dense(c, q, out, lse)
+
+
+def test_tiny_values_of_an_8bit_cache():
+    """Value rows at the smallest exponents (their values are 2^-126 times whole numbers)."""
+    build.build()
+    c = Paged([200], 1, 2, 32, True, seed=12)
+    c.v_exp[c.v_exp != 255] = 10
+    q = c.queries(1)
+    out, lse = dense(c, q)
+    status_ok()
+    o = torch.zeros(2, D, dtype=torch.float64, device="cuda")
+    pos = torch.arange(200, device="cuda")
+    from page_helpers import attend_ref
+    o, _, tol, _ = attend_ref(q[0], c.rows("k", 0, 0, pos), c.rows("v", 0, 0, pos), SCALE)
+    # fp32 results below 2^-126 have an absolute step of 2^-149: a few of them.
+    assert ((out[0].double() - o).abs() <= tol + 2.0 ** -146).all() and (out != 0).any()
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("lens,G,gs,P", SHAPES)
+def test_dense_writes_the_newest_row(lens, G, gs, P, kv8):
+    """k_new, v_new land in the newest position and nowhere else, and are attended to."""
+    build.build()
+    c = Paged(lens, G, gs, P, kv8, seed=21 + P)
+    B = len(lens)
+    k_new = torch.randn(B, G, D, device="cuda").bfloat16() * 3
+    v_new = torch.randn(B, G, D, device="cuda").bfloat16() * 2
+    want = [x.clone() if x is not None else None for x in (c.k, c.v, c.k_exp, c.v_exp)]
+    for b, n in enumerate(lens):
+        if n == 0:
+            continue
+        phys, slot = int(c.pt[b, (n - 1) // P]), (n - 1) % P
+        for i, x in ((0, k_new), (1, v_new)):
+            if kv8:
+                y, e = quantise_ref(x[b])
+                want[i][phys, :, slot], want[i + 2][phys, :, slot] = y.cuda(), e.cuda()
+            else:
+                want[i][phys, :, slot] = x[b]
+    q = c.queries(B)
+    out, lse = dense(c, q, k_new=k_new, v_new=v_new)
+    status_ok()
+    for got, ref in zip((c.k, c.v, c.k_exp, c.v_exp), want):
+        if ref is not None:
+            bits = torch.uint8 if kv8 else torch.int16
+            assert torch.equal(got.view(bits), ref.view(bits))
+    check_dense(c, q, out, lse)
+
+
+def blocks_of(c, T, rows, m, seed, pos):
+    """Random block lists: unsorted, one block twice, some lists empty or shorter than m."""
+    gen = torch.Generator().manual_seed(seed)
+    B = len(c.lens)
+    blocks = torch.full((B, T, rows, m), 1 << 20, dtype=torch.int32)  # past the count: anything
+    count = torch.zeros(B, T, rows, dtype=torch.int32)
+    for b in range(B):
+        n_pages = -(-c.lens[b] // c.P)
+        for t in range(T):
+            for r in range(rows):
+                k = int(torch.randint(0, m + 1, (1,), generator=gen)) if n_pages else 0
+                pick = torch.randint(0, max(n_pages, 1), (k,), generator=gen)
+                if k >= 2:
+                    pick[k // 2] = pick[0]
+                blocks[b, t, r, :k] = pick.int()
+                count[b, t, r] = k
+    return blocks.cuda(), count.cuda()
+
+
+def sparse(c, q, blocks, count, q_pos, out_dtype=torch.float32):
+    out = torch.full(q.shape, math.nan, dtype=out_dtype, device="cuda")
+    lse = torch.full(q.shape[:-1], math.nan, device="cuda")
+    ws = torch.full((hhr.hhr_block_attn_workspace_bytes(c.d, q.shape[1], blocks.shape[-1]),), 0xff,
+                    dtype=torch.uint8, device="cuda")
+    hhr.hhr_block_attn(c.d, q, c.k, c.v, c.k_exp, c.v_exp, c.pt, c.seq_len, q_pos, blocks, count,
+                       SCALE, out, ws, lse=lse)
+    return out, lse
+
+
+def check_sparse(c, q, blocks, count, q_pos, out, lse):
+    rows = blocks.shape[2]
+    gs = c.G * c.gs // rows
+    for b, n in enumerate(c.lens):
+        for t in range(q.shape[1]):
+            limit = n if q_pos is None else min(n, int(q_pos[b, t]) + 1)
+            for r in range(rows):
+                chosen = blocks[b, t, r, :int(count[b, t, r])].long()
+                pos = (chosen[:, None] * c.P + torch.arange(c.P, device="cuda")).reshape(-1)
+                pos = pos[pos < limit]
+                h, g = slice(r * gs, (r + 1) * gs), r * c.G // rows
+                check_rows(out[b, t, h], lse[b, t, h], q[b, t, h], c.rows("k", b, g, pos),
+                           c.rows("v", b, g, pos), SCALE, f"sequence {b}, query {t}, row {r}")
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("lens,G,gs,P,T,m,causal", [
+    ([1], 1, 1, 1, 1, 1, False),
+    ([700, 0, 33], 2, 4, 32, 1, 5, False),
+    ([700, 90, 33], 2, 3, 17, 4, 3, True),
+    ([2000], 8, 4, 128, 16, 4, True),
+    ([4000, 3999], 1, 8, 64, 1, 40, False),
+    ([513], 3, 5, 5, 9, 60, True),
+    ([300, 260], 2, 7, 256, 2, 2, True),
+])
+def test_blocks(lens, G, gs, P, T, m, causal, kv8, per_head):
+    build.build()
+    c = Paged(lens, G, gs, P, kv8, seed=31 + P)
+    c.d.select_per_head = int(per_head)
+    rows = G * gs if per_head else G
+    q = c.queries(len(lens), T)
+    # Positions from before the first key to past the last.
+    q_pos = (torch.linspace(-1, max(lens) + 3, T, device="cuda").int().expand(len(lens), T)
+             .contiguous() if causal else None)
+    blocks, count = blocks_of(c, T, rows, m, 7 * P + T, q_pos)
+    for dtype in (torch.float32, torch.bfloat16):
+        out, lse = sparse(c, q, blocks, count, q_pos, dtype)
+        status_ok()
+        check_sparse(c, q, blocks, count, q_pos, out, lse)
+
+
+def test_every_block_listed_equals_dense_attention():
+    """All pages listed in order: the same sums as the dense call, up to their split."""
+    build.build()
+    for kv8 in (False, True):
+        c = Paged([3001], 2, 4, 32, kv8, seed=41)
+        q = c.queries(1)
+        n = -(-3001 // 32)
+        blocks = torch.arange(n, dtype=torch.int32, device="cuda").expand(1, 1, 2, n).contiguous()
+        count = torch.full((1, 1, 2), n, dtype=torch.int32, device="cuda")
+        out, lse = sparse(c, q[:, None], blocks, count, None)
+        status_ok()
+        check_dense(c, q, out[:, 0], lse[:, 0])
+
+
+def test_joining_two_halves_by_their_lse():
+    """Outputs over disjoint block sets, joined by their log-sums, are those over the union."""
+    build.build()
+    c = Paged([2048], 2, 4, 32, False, seed=51)
+    q = c.queries(1, 1)
+    parts = []
+    for lo, hi in ((0, 20), (20, 64), (0, 64)):
+        blocks = torch.arange(lo, hi, dtype=torch.int32, device="cuda").expand(1, 1, 2, hi - lo)
+        count = torch.full((1, 1, 2), hi - lo, dtype=torch.int32, device="cuda")
+        parts.append(sparse(c, q, blocks.contiguous(), count, None))
+    status_ok()
+    (o1, l1), (o2, l2), (o, l) = parts
+    both = torch.logaddexp(l1, l2)
+    joined = o1 * (l1 - both).exp()[..., None] + o2 * (l2 - both).exp()[..., None]
+    check_dense(c, q[:, 0], joined[:, 0], both[:, 0])
+    check_dense(c, q[:, 0], o[:, 0], l[:, 0])
+
+
+def test_equal_inputs_give_equal_bits_on_any_stream_and_in_a_graph():
+    build.build()
+    c = Paged([9000, 77, 3000], 4, 4, 32, True, seed=61)
+    q = c.queries(3)
+    out, lse = dense(c, q)
+    ref = out.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other, _ = dense(c, q)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(other, ref)
+    ws = torch.empty(hhr.hhr_paged_attn_workspace_bytes(c.d), dtype=torch.uint8, device="cuda")
+    got, l2 = torch.empty_like(out), torch.empty_like(lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        hhr.hhr_paged_attn(c.d, q, None, None, c.k, c.v, c.k_exp, c.v_exp, c.pt, c.seq_len, SCALE,
+                           got, ws, lse=l2)
+    for _ in range(3):
+        got.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref) and torch.equal(l2, lse)
+    # Other lengths and queries through the same graph: nothing of the first call is kept.
+    c.lens = [1, 5000, 0]
+    c.pt[1, :] = c.pt[0, :]
+    c.seq_len.copy_(torch.tensor(c.lens))
+    q.copy_(c.queries(3))
+    graph.replay()
+    status_ok()
+    check_dense(c, q, got, l2)
+
+
+def test_bad_pages_and_blocks_are_skipped_and_flagged():
+    build.build()
+    for kv8 in (False, True):
+        c = Paged([200, 200], 1, 2, 32, kv8, seed=71)
+        q = c.queries(2)
+        good = c.pt.clone()
+        c.pt[0, 2] = c.n_phys + 5
+        c.pt[1, 0] = -3
+        out, lse = dense(c, q)
+        torch.cuda.synchronize()
+        assert hhr.hhr_read_device_status() == (hhr.HHR_ERR_DEVICE_STATUS, 1)
+        bad, c.pt = c.pt, good
+        for b, skip in ((0, 2), (1, 0)):
+            pos = torch.arange(200, device="cuda")
+            pos = pos[pos // 32 != skip]
+            check_rows(out[b], lse[b], q[b], c.rows("k", b, 0, pos), c.rows("v", b, 0, pos), SCALE, "skip")
+        # A length beyond the page table is clipped.
+        c.seq_len[1] = c.maxp * 32 + 1
+        c.pt[1, -1] = c.pt[0, 0]
+        c.pt[1, -2] = c.pt[0, 1]
+        dense(c, q)
+        torch.cuda.synchronize()
+        assert hhr.hhr_read_device_status() == (hhr.HHR_ERR_DEVICE_STATUS, 2)
+        c.seq_len[1] = 200
+        blocks = torch.tensor([[[[1, -1, 3]]], [[[c.maxp, 0, 2]]]], dtype=torch.int32, device="cuda")
+        count = torch.full((2, 1, 1), 3, dtype=torch.int32, device="cuda")
+        out, lse = sparse(c, q[:, None], blocks, count, None)
+        torch.cuda.synchronize()
+        assert hhr.hhr_read_device_status() == (hhr.HHR_ERR_DEVICE_STATUS, 2)
+        for b, keep in ((0, (1, 3)), (1, (0, 2))):
+            pos = torch.cat([torch.arange(32 * p, 32 * p + 32, device="cuda") for p in keep])
+            check_rows(out[b, 0], lse[b, 0], q[b], c.rows("k", b, 0, pos), c.rows("v", b, 0, pos), SCALE, "skip")
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_nan_and_infinite_keys_act_on_their_heads_only(kv8):
+    """A NaN in a key makes its row NaN and no other; a value's NaN likewise its channel."""
+    build.build()
+    c = Paged([300, 300], 2, 2, 32, kv8, seed=81)
+    phys = int(c.pt[0, 1])
+    if kv8:
+        c.k[phys, 0, 3, 5] = 0x7f
+        c.v[phys, 1, 3, 9] = 0x7f
+    else:
+        c.k[phys, 0, 3, 5] = math.nan
+        c.v[phys, 1, 3, 9] = math.nan
+    q = c.queries(2)
+    out, lse = dense(c, q)
+    status_ok()
+    assert torch.isnan(out[0, :2]).all() and torch.isnan(lse[0, :2]).all()
+    assert torch.isnan(out[0, 2:, 9]).all()
+    clean = torch.arange(D, device="cuda") != 9
+    assert torch.isfinite(out[0, 2:][:, clean]).all() and torch.isfinite(out[1]).all()
+    assert torch.isfinite(lse[0, 2:]).all() and torch.isfinite(lse[1]).all()
+
+
+def test_cache_rows_past_2_to_31_bytes():
+    """Pages whose byte offsets pass 32 bits (a 9 GB pool), the sequence lying at its end."""
+    build.build()
+    P, G, n_phys = 256, 8, 8200                    # 8200 * 8 * 256 rows of 256 bytes: 4.3 GB
+    k = torch.empty(n_phys, G, P, D, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    c = Paged([700], G, 4, P, False, seed=91)
+    for j in range(3):
+        src = int(c.pt[0, j])
+        k[n_phys - 1 - j], v[n_phys - 1 - j] = c.k[src], c.v[src]
+        c.pt[0, j] = n_phys - 1 - j
+    c.k, c.v, c.n_phys = k, v, n_phys
+    c.d.n_phys_pages = n_phys
+    q = c.queries(1)
+    out, lse = dense(c, q)
+    status_ok()
+    check_dense(c, q, out, lse)
