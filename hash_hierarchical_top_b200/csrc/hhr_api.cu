@@ -118,6 +118,9 @@ int sm_count() {
   return cached[dev];
 }
 
+// Dynamic shared memory that every kernel of this file may ask for once its limit has been
+// raised: the 227 KB opt-in of sm_100 less 16 KB, more than any kernel's static shared memory.
+constexpr size_t kAlwaysSmem = (227 - 16) * 1024;
 // Raise a kernel's dynamic shared-memory limit (opt-in maximum minus the kernel's
 // static shared memory) once per device, and check that `bytes` fits under it.
 template <typename K>
@@ -126,6 +129,7 @@ cudaError_t allow_smem(K kernel, size_t bytes, bool* done_per_dev) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return g_last_cuda = e;
   if (dev < 0 || dev >= kMaxDevices) return g_last_cuda = cudaErrorInvalidDevice;
+  if (done_per_dev[dev] && bytes <= kAlwaysSmem) return cudaSuccess;
   cudaFuncAttributes fa;
   if ((e = cudaFuncGetAttributes(&fa, kernel)) != cudaSuccess) return g_last_cuda = e;
   int optin = 0;
@@ -956,7 +960,7 @@ int hhr_read_device_status(void* stream, int* bits) {
 
 namespace {
 
-bool g_smem_topm[kMaxDevices];
+bool g_smem_page[2][2][kMaxDevices], g_smem_topm[kMaxDevices], g_smem_tile[kMaxDevices];
 
 // Cache rows are addressed with 32-bit row indices.
 bool rows_fit(const hhr_dims* d) {
@@ -1005,13 +1009,14 @@ int launch_page_attn(const hhr_dims* d, PageAttnArgs& a, bool k8, long long unit
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                        align256((size_t)2 * a.n_ctas * gs * kD * 4));
   void (*k)(PageAttnArgs) = k8 ? page_attn_kernel<true, kList> : page_attn_kernel<false, kList>;
+  if (allow_smem(k, page_attn_smem(), g_smem_page[k8][kList]) != cudaSuccess) return HHR_ERR_CUDA;
   prof_begin(HHR_KERNEL_PAGE, s);
   k<<<a.n_ctas, kPaThreads, page_attn_smem(), s>>>(a);
   prof_end(HHR_KERNEL_PAGE, s);
   int st = launch_status();
   if (st != HHR_OK) return st;
   prof_begin(HHR_KERNEL_JOIN, s);
-  const cudaError_t e = launch_pdl(page_join_kernel<kList>, dim3((unsigned)(a.B * a.T * a.Gs)),
+  const cudaError_t e = launch_pdl(page_join_kernel<kList>, dim3((unsigned)(a.B * a.T * a.Gs), (unsigned)gs),
                                    dim3(kJoinThreads), 0, s, a);
   prof_end(HHR_KERNEL_JOIN, s);
   if (e != cudaSuccess) { g_last_cuda = e; return HHR_ERR_CUDA; }
@@ -1168,11 +1173,21 @@ int hhr_block_select(const hhr_dims* d, int n_queries, const uint16_t* q, const 
                     kv_div(d), d->page_size, maxp, d->n_phys_pages, m_pages,
                     kept_max(d, m_pages, 0), sink, local};
   const size_t smem = (size_t)maxp * 4;
+  // Rows of one KV group, and their tiles over all groups.
+  const long long rows = (long long)n_queries * a.kv_div;
+  const long long tiles = (rows + kBtRows - 1) / kBtRows * d->n_kv_heads;
+  if (tiles > 65535) return HHR_ERR_UNSUPPORTED;
+  if (rows > 1 && allow_smem(block_mean_tile_kernel, block_tile_smem(), g_smem_tile) != cudaSuccess)
+    return HHR_ERR_CUDA;
   if (smem > kDefaultSmem && allow_smem(block_topm_kernel, smem, g_smem_topm) != cudaSuccess)
     return HHR_ERR_CUDA;
   prof_begin(HHR_KERNEL_MEAN, s);
-  block_mean_score_kernel<<<dim3((maxp + kBsPages - 1) / kBsPages, d->n_kv_heads, B), kBsThreads,
-                            0, s>>>(a);
+  if (rows == 1)
+    block_mean_stream_kernel<<<dim3((maxp + kBvWarps * 32 - 1) / (kBvWarps * 32), d->n_kv_heads, B),
+                               kBvWarps * 32, 0, s>>>(a);
+  else
+    block_mean_tile_kernel<<<dim3((maxp + kBtPages - 1) / kBtPages, (unsigned)tiles, B), kBtThreads,
+                             block_tile_smem(), s>>>(a);
   prof_end(HHR_KERNEL_MEAN, s);
   if ((st = launch_status()) != HHR_OK) return st;
   prof_begin(HHR_KERNEL_TOPM, s);

@@ -43,10 +43,23 @@
 
 namespace hhr {
 
-constexpr int kPaWarps = 8;
+#ifndef HHR_PA_WARPS
+#define HHR_PA_WARPS 4
+#endif
+#ifndef HHR_PA_CTAS
+#define HHR_PA_CTAS 2
+#endif
+#ifndef HHR_PA_UNIT
+#define HHR_PA_UNIT 128
+#endif
+#ifndef HHR_PA_STAGES
+#define HHR_PA_STAGES 3
+#endif
+constexpr int kPaStages = HHR_PA_STAGES;
+constexpr int kPaWarps = HHR_PA_WARPS;
 constexpr int kPaThreads = kPaWarps * 32;
-constexpr int kPaCtasPerSm = 2;
-constexpr int kUnitKeys = 128;
+constexpr int kPaCtasPerSm = HHR_PA_CTAS;
+constexpr int kUnitKeys = HHR_PA_UNIT;
 
 struct PageAttnArgs {
   const uint16_t* q;      // [B][T][Hq][d]
@@ -94,52 +107,55 @@ __device__ __forceinline__ int share_of(int u, int total, int n) {
   return (int)((((long long)u + 1) * n - 1) / total);
 }
 
-// Block-wide (256 threads): the sum of units over sequences [0, B) of dense rows, each counted
-// Gs times, and either the place of unit `find` (find >= 0: *at_b, the sequence, *at_u the units
-// before it inside that sequence) or the units before sequence -1 - find (*at_u). sh: 40 ints.
-__device__ __forceinline__ int dense_scan(const PageAttnArgs& a, int find, int* sh, int* at_b,
-                                          int* at_u) {
-  const int tid = threadIdx.x, per = (a.B + blockDim.x - 1) / blockDim.x;
+// Where a place of the dense rows' units lies: sequence b, `before` units ahead of it, and all
+// the units of the call.
+struct DensePlace {
+  int total, b, before;
+};
+// Block-wide: a.B sequences, each counted Gs times. pick(total) is the unit that is looked for
+// (>= 0), or -1 - b for the place of sequence b. Up to 32 sequences every warp scans them on its
+// own, without a barrier; else the block does. sh: 40 ints.
+template <typename Pick>
+__device__ __forceinline__ DensePlace dense_place(const PageAttnArgs& a, int* sh, Pick pick) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  DensePlace r;
+  if (a.B <= 32) {
+    const int u = lane < a.B ? units_of(dense_len(a, lane)) * a.Gs : 0;
+    const int incl = warp_incl_scan(u, lane);
+    r.total = __shfl_sync(kFull, incl, 31);
+    const int want = pick(r.total);
+    // The first sequence whose units end behind the wanted one.
+    r.b = want >= 0 ? __ffs(__ballot_sync(kFull, incl > want)) - 1 : -1 - want;
+    r.before = __shfl_sync(kFull, incl - u, r.b);
+    return r;
+  }
+  const int per = (a.B + blockDim.x - 1) / blockDim.x;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   int sum = 0;
   for (int b = b0; b < b1; ++b) sum += units_of(dense_len(a, b)) * a.Gs;
-  int total;
-  int before = block_excl_scan<true>(sum, sh, &total);
-  if (find >= 0) {
-    if (find >= before && find < before + sum) {
-      int b = b0;
-      for (; b < b1 - 1; ++b) {
-        const int u = units_of(dense_len(a, b)) * a.Gs;
-        if (find < before + u) break;
-        before += u;
-      }
-      sh[36] = b;
-      sh[37] = find - before;
+  int before = block_excl_scan(sum, sh, &r.total);
+  const int want = pick(r.total);
+  if (want >= 0 ? (want >= before && want < before + sum) : (-1 - want >= b0 && -1 - want < b1)) {
+    int b = b0;
+    while (true) {
+      const int u = units_of(dense_len(a, b)) * a.Gs;
+      if (want >= 0 ? want < before + u : b == -1 - want) break;
+      before += u;
+      ++b;
     }
-  } else {
-    const int want = -1 - find;
-    if (want >= b0 && want < b1) {
-      for (int b = b0; b < want; ++b) before += units_of(dense_len(a, b)) * a.Gs;
-      sh[36] = want;
-      sh[37] = before;
-    }
+    sh[36] = b;
+    sh[37] = before;
   }
   __syncthreads();
-  *at_b = sh[36];
-  *at_u = sh[37];
-  return total;
+  r.b = sh[36];
+  r.before = sh[37];
+  return r;
 }
 
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
+// 16 bytes into shared memory; n = 0 writes zeros and reads nothing.
+__device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n)
                : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
 // f16 counterpart of mma_16816, and the f16 packing of two floats.
@@ -207,54 +223,102 @@ __device__ __forceinline__ uint32_t row_of(const PageAttnArgs& a, const RowKeys&
   return ((uint32_t)phys * (uint32_t)a.G + r.g) * (uint32_t)a.P + (uint32_t)slot;
 }
 
+// Shared memory of one warp: kPaStages stages of a K tile and a V tile, S rows each (16 bf16 or
+// 32 8-bit rows: 4 KB a tile). The 16-byte chunks of a row are XOR-swizzled by row % 8, so that
+// ldmatrix reads of 8 rows hit 8 distinct bank groups.
+constexpr int kPaTile = 4096;
+constexpr int kPaRing = kPaStages * 2 * kPaTile;
+
 // Keys [k0, k1) of a row, over the CTA's warps: the state of every head is left in shared
-// memory (mo [warps][8][d], ml [warps][8][2]).
+// memory (mo [warps][8][d], ml [warps][8][2], which reuse the rings). Ends with the state of
+// all warps written (a barrier).
 template <bool K8, bool kList>
 __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKeys& rk,
-                                             const uint16_t* q, int gs, int k0, int k1, float* mo,
-                                             float* ml) {
-  constexpr int S = K8 ? 32 : 16;   // keys of a warp's step
-  constexpr int NT = S / 8;         // 8-key tiles of S
+                                             const uint16_t* q, int gs, int k0, int k1,
+                                             char* smem, float* mo, float* ml) {
+  constexpr int S = K8 ? 32 : 16;       // keys of a warp's step
+  constexpr int NT = S / 8;             // 8-key tiles of S
   constexpr int RB = K8 ? kD : 2 * kD;  // bytes of a cache row
+  constexpr int RC = RB / 16;           // 16-byte chunks of a row
+  constexpr int NS = kPaStages;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gq = lane >> 2, tq = lane & 3;
   const char* kb = reinterpret_cast<const char*>(a.k);
   const char* vb = reinterpret_cast<const char*>(a.v);
+  const uint32_t ring = smem_u32(smem) + (uint32_t)warp * kPaRing;
+  const int base = k0 + warp * S, stride = kPaWarps * S;
+  const int lk = K8 ? lane : (lane & 15);  // the key of a step that this lane locates
 
-  // Query fragments: MMA (c, s) takes the channels [ch, ch + 4) of lane tq, ch = (16 or 8)
-  // (tq + 4c) + 4s, as k = 2tq, 2tq + 1, 2tq + 8, 2tq + 9.
+  auto block_at = [&](int j) { return j < k1 ? block_of<kList>(a, rk, j) : -1; };
+  // Copies the rows of a step (`row`: this lane's) into stage st; missing rows become zeros.
+  auto issue = [&](uint32_t row, int st) {
+    const uint32_t ks = ring + (uint32_t)st * 2 * kPaTile;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = i * (32 / RC) + lane / RC, c = lane % RC;
+      const uint32_t o = __shfl_sync(kFull, row, r);
+      const uint32_t n = o != kNoRow ? 16u : 0u;
+      const size_t off = o != kNoRow ? (size_t)o * RB + 16 * c : 0;
+      const uint32_t dst = ks + (uint32_t)(r * RB + ((c ^ (r & 7)) << 4));
+      cp_async16_zfill(dst, kb + off, n);
+      cp_async16_zfill(dst + kPaTile, vb + off, n);
+    }
+  };
+
+  // rq[i]: the row this lane locates in step i from now. Page ids are loaded one step before
+  // the row index is needed, block ids one step before that.
+  uint32_t rq[NS];
+  int j0 = base + lk, blk1, phys1, blk2;
+  {
+    int bl[NS + 1], ph[NS];
+#pragma unroll
+    for (int i = 0; i <= NS; ++i) bl[i] = block_at(j0 + i * stride);
+#pragma unroll
+    for (int i = 0; i < NS; ++i) ph[i] = phys_of(a, rk, bl[i]);
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i) {
+      rq[i] = row_of(a, rk, j0 + i * stride, bl[i], ph[i]);
+      issue(rq[i], i);
+      cp_async_commit();
+    }
+    blk1 = bl[NS - 1];
+    phys1 = ph[NS - 1];
+    blk2 = bl[NS];
+    j0 += (NS - 1) * stride;
+  }
+  // 8-bit: the exponent bytes of the row that this lane locates (K low, V next).
+  auto exponents = [&](uint32_t row) {
+    return row != kNoRow ? (uint32_t)a.k_exp[row] | (uint32_t)a.v_exp[row] << 8 : 0u;
+  };
+  uint32_t ex = K8 ? exponents(rq[0]) : 0u;
+
+  // Query fragments (rows >= gs zero). bf16: MMA i takes the channels 16i..16i+15 in order;
+  // 8-bit: k = 2tq, 2tq + 1, 2tq + 8, 2tq + 9 are the channels 16i + 4tq + {0, 1, 2, 3}.
   uint32_t qa[8][2];
   float hs = a.scale_log2;
   {
     const bool hv = gq < gs;
-    const uint2* q4 = reinterpret_cast<const uint2*>(q + (size_t)(hv ? gq : 0) * kD);
-    uint2 w[8];
+    const uint32_t* q2 = reinterpret_cast<const uint32_t*>(q + (size_t)(hv ? gq : 0) * kD);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int ch = K8 ? 16 * (tq + 4 * (i >> 2)) + 4 * (i & 3) : 8 * (tq + 4 * (i >> 1)) + 4 * (i & 1);
-      w[i] = hv ? q4[ch >> 2] : make_uint2(0u, 0u);
+      qa[i][0] = hv ? q2[8 * i + (K8 ? 2 * tq : tq)] : 0u;
+      qa[i][1] = hv ? q2[8 * i + (K8 ? 2 * tq + 1 : tq + 4)] : 0u;
     }
     if constexpr (K8) {
       uint32_t top = 0u;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        top = max(max(top, max(w[i].x & 0x7fffu, (w[i].x >> 16) & 0x7fffu)),
-                  max(w[i].y & 0x7fffu, (w[i].y >> 16) & 0x7fffu));
+        top = max(max(top, max(qa[i][0] & 0x7fffu, (qa[i][0] >> 16) & 0x7fffu)),
+                  max(qa[i][1] & 0x7fffu, (qa[i][1] >> 16) & 0x7fffu));
       top = max(top, __shfl_xor_sync(kFull, top, 1));
       top = max(top, __shfl_xor_sync(kFull, top, 2));
-      const uint32_t E = max(top >> 7, 15u);          // exponent field of the largest channel
+      const uint32_t E = max(top >> 7, 15u);               // exponent field of the largest channel
       const float up = __uint_as_float((268u - E) << 23);  // 2^(14 - (E - 127))
       hs = a.scale_log2 * __uint_as_float((E - 14u) << 23);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        qa[i][0] = pack_f16(bf16_lo(w[i].x) * up, bf16_hi(w[i].x) * up);
-        qa[i][1] = pack_f16(bf16_lo(w[i].y) * up, bf16_hi(w[i].y) * up);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        qa[i][0] = w[i].x;
-        qa[i][1] = w[i].y;
+        qa[i][0] = pack_f16(bf16_lo(qa[i][0]) * up, bf16_hi(qa[i][0]) * up);
+        qa[i][1] = pack_f16(bf16_lo(qa[i][1]) * up, bf16_hi(qa[i][1]) * up);
       }
     }
   }
@@ -264,77 +328,45 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
   float oacc[8][4];
 #pragma unroll
   for (int i = 0; i < 8; ++i) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.f;
+  const int l8 = lane & 7, mj = lane >> 3;  // ldmatrix: row and matrix that this lane addresses
 
-  uint4 kf[8], vf[8];
-  uint32_t ex = 0u;  // 8-bit: exponent bytes of this lane's key (K low, V next)
-  const int base = k0 + warp * S, stride = kPaWarps * S;
-  const int lk = K8 ? lane : (lane & 15);  // the key of a step that this lane locates
-
-  auto load_k = [&](uint32_t row) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const uint32_t o = __shfl_sync(kFull, row, 8 * j + gq);
-      const char* p = kb + (size_t)o * RB + 16 * tq;
-#pragma unroll
-      for (int c = 0; c < 8 / NT; ++c)
-        kf[j * (8 / NT) + c] = o != kNoRow ? ldg_stream(p + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
-    }
-    if constexpr (K8) ex = row != kNoRow ? (uint32_t)a.k_exp[row] | (uint32_t)a.v_exp[row] << 8 : 0u;
-  };
-  // vf: bf16: [key of 2t, 2t+1, 2t+8, 2t+9][piece gq, gq + 8]; 8-bit: [16-key group][key], piece gq.
-  auto load_v = [&](uint32_t row) {
-#pragma unroll
-    for (int i = 0; i < S / 4; ++i) {
-      const int key = 16 * (i >> 2) + 8 * ((i >> 1) & 1) + (i & 1) + 2 * tq;
-      const uint32_t o = __shfl_sync(kFull, row, key);
-      const char* p = vb + (size_t)o * RB + 16 * gq;
-      if constexpr (K8) {
-        vf[i] = o != kNoRow ? ldg_stream(p) : make_uint4(0u, 0u, 0u, 0u);
-      } else {
-        vf[2 * i] = o != kNoRow ? ldg_stream(p) : make_uint4(0u, 0u, 0u, 0u);
-        vf[2 * i + 1] = o != kNoRow ? ldg_stream(p + 128) : make_uint4(0u, 0u, 0u, 0u);
-      }
-    }
-  };
-  auto block_at = [&](int j) { return j < k1 ? block_of<kList>(a, rk, j) : -1; };
-
-  int j0 = base + lk;
-  int blk = block_at(j0);
-  uint32_t row = row_of(a, rk, j0, blk, phys_of(a, rk, blk));
-  int blk1 = block_at(j0 + stride);
-  int phys1 = phys_of(a, rk, blk1);
-  int blk2 = block_at(j0 + 2 * stride);
-  load_k(row);
-  load_v(row);
-  uint32_t ex_cur = ex;
+  int st = 0;
   for (int s0 = base; s0 < k1; s0 += stride, j0 += stride) {
-    // The next step's rows, and the page ids of the one after.
-    const uint32_t row_next = row_of(a, rk, j0 + stride, blk1, phys1);
+    cp_async_wait<NS - 2>();
+    __syncwarp();  // the stage's rows are there; the previous step's stage has been read
+    // The rows of NS - 1 steps ahead, and the page ids of the step after it.
+    rq[NS - 1] = row_of(a, rk, j0, blk1, phys1);
+    issue(rq[NS - 1], st == 0 ? NS - 1 : st - 1);
+    cp_async_commit();
     blk1 = blk2;
     phys1 = phys_of(a, rk, blk1);
-    blk2 = block_at(j0 + 3 * stride);
-    const bool more = s0 + stride < k1;
+    blk2 = block_at(j0 + 2 * stride);
+    const uint32_t ks = ring + (uint32_t)st * 2 * kPaTile, vs = ks + kPaTile;
+    const unsigned ok = __ballot_sync(kFull, rq[0] != kNoRow);
 
     float sacc[NT][4];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
+      float s2[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of 4: less truncation, and overlap
       sacc[j][0] = sacc[j][1] = sacc[j][2] = sacc[j][3] = 0.f;
+      const int r = 8 * j + l8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int c = 0; c < RC; c += 4) {  // 4 chunks of 8 keys at a time
+        uint32_t w[4];
+        ldsm_x4(ks + (uint32_t)(r * RB + (((c + mj) ^ l8) << 4)), w[0], w[1], w[2], w[3]);
         if constexpr (K8) {
-          const uint32_t w = word_of(kf[2 * j + (i >> 2)], i & 3);
-          mma_16816_f16(sacc[j], qa[i][0], 0u, qa[i][1], 0u, e4m3x2_to_f16x2(w & 0xffffu),
-                        e4m3x2_to_f16x2(w >> 16));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            mma_16816_f16((i & 1) ? s2 : sacc[j], qa[c + i][0], 0u, qa[c + i][1], 0u,
+                          e4m3x2_to_f16x2(w[i] & 0xffffu), e4m3x2_to_f16x2(w[i] >> 16));
         } else {
-          const uint4& w = kf[4 * j + (i >> 1)];
-          mma_16816(sacc[j], qa[i][0], 0u, qa[i][1], 0u, word_of(w, 2 * (i & 1)),
-                    word_of(w, 2 * (i & 1) + 1));
+          mma_16816(sacc[j], qa[c / 2][0], 0u, qa[c / 2][1], 0u, w[0], w[1]);
+          mma_16816(s2, qa[c / 2 + 1][0], 0u, qa[c / 2 + 1][1], 0u, w[2], w[3]);
         }
       }
+      sacc[j][0] += s2[0];
+      sacc[j][1] += s2[1];
     }
-    const unsigned ok = __ballot_sync(kFull, row != kNoRow);
-    ex_cur = ex;
-    if (more) load_k(row_next);
 
     // Logits in log2 units, of head gq and the keys 8j + 2tq, 8j + 2tq + 1.
     float mx = -INFINITY;
@@ -346,7 +378,7 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
         const int key = 8 * j + 2 * tq + i;
         float sc = hs;
         if constexpr (K8) {
-          e2[j][i] = __shfl_sync(kFull, ex_cur, key);
+          e2[j][i] = __shfl_sync(kFull, ex, key);
           sc *= exp_scale(e2[j][i] & 0xffu);
         }
         sacc[j][i] = (ok >> key & 1u) ? sacc[j][i] * sc : -INFINITY;
@@ -356,25 +388,19 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
     const float m_new = fmaxf(m_run, mx);
-    uint32_t e_new = e_run;
-    if constexpr (K8) e_new = max(e_run, __reduce_max_sync(kFull, ex_cur >> 8));
-    if (__any_sync(kFull, m_new > m_run) || e_new != e_run) {
-      const float c = m_new > m_run ? exp2f(m_run - m_new) : 1.f;
-      l_run *= c;
-      float ca = __shfl_sync(kFull, c, 8 * tq), cb = __shfl_sync(kFull, c, 8 * tq + 4);
-      if constexpr (K8) {
-        const float ec = exp_scale((uint32_t)max(127 + (int)e_run - (int)e_new, 0));
-        ca *= ec;
-        cb *= ec;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        oacc[i][0] *= ca; oacc[i][2] *= ca;
-        oacc[i][1] *= cb; oacc[i][3] *= cb;
-      }
-      m_run = m_new;
+    // What the sums so far are scaled by: head gq's, and those of the columns 2tq, 2tq + 1.
+    const float corr = m_new > m_run ? exp2f(m_run - m_new) : 1.f;
+    l_run *= corr;
+    float ca = __shfl_sync(kFull, corr, 8 * tq), cb = __shfl_sync(kFull, corr, 8 * tq + 4);
+    if constexpr (K8) {
+      const uint32_t e_new = max(e_run, __reduce_max_sync(kFull, ex >> 8));
+      const float ec = exp_scale((uint32_t)max(127 + (int)e_run - (int)e_new, 0));
+      ca *= ec;
+      cb *= ec;
       e_run = e_new;
+      ex = exponents(rq[1]);
     }
+    m_run = m_new;
     const float mu = m_run == -INFINITY ? 0.f : m_run;
     uint32_t ph[NT], pl[NT];
 #pragma unroll
@@ -389,36 +415,43 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
       }
       split_pair<K8>(p[0], p[1], ph[j], pl[j]);
     }
-    // O^T += V^T P^T, 16 keys at a time.
+    // O^T = corr O^T + V^T P^T. The step's products are summed from zero and added in fp32: the
+    // matrix units truncate when they add to an accumulator, and over thousands of steps that
+    // is a bias (8e-6 of the output at 128K keys; 1e-6 this way).
 #pragma unroll
-    for (int h = 0; h < S / 16; ++h) {
+    for (int i = 0; i < 8; ++i) {
+      float o[4] = {0.f, 0.f, 0.f, 0.f};
+      uint32_t w[4];
+      if constexpr (K8) {
+        // Chunk i of 32 keys: register k holds, for the keys 8k + 2tq and 8k + 2tq + 1, the
+        // channels 16i + 2gq and 16i + 2gq + 1 (rows gq and gq + 8 of A).
+        ldsm_x4_t(vs + (uint32_t)(lane * RB + ((i ^ l8) << 4)), w[0], w[1], w[2], w[3]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t a0, a1, a2, a3;
-        if constexpr (K8) {
-          const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
-          const uint32_t x = __byte_perm(word_of(vf[4 * h], i >> 1), word_of(vf[4 * h + 1], i >> 1), sel);
-          const uint32_t y = __byte_perm(word_of(vf[4 * h + 2], i >> 1), word_of(vf[4 * h + 3], i >> 1), sel);
-          a0 = e4m3x2_to_f16x2(x & 0xffffu);
-          a1 = e4m3x2_to_f16x2(x >> 16);
-          a2 = e4m3x2_to_f16x2(y & 0xffffu);
-          a3 = e4m3x2_to_f16x2(y >> 16);
-          mma_16816_f16(oacc[i], a0, a1, a2, a3, ph[2 * h], ph[2 * h + 1]);
-          mma_16816_f16(oacc[i], a0, a1, a2, a3, pl[2 * h], pl[2 * h + 1]);
-        } else {
-          const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u;
-          a0 = __byte_perm(word_of(vf[0], i >> 1), word_of(vf[2], i >> 1), sel);
-          a1 = __byte_perm(word_of(vf[1], i >> 1), word_of(vf[3], i >> 1), sel);
-          a2 = __byte_perm(word_of(vf[4], i >> 1), word_of(vf[6], i >> 1), sel);
-          a3 = __byte_perm(word_of(vf[5], i >> 1), word_of(vf[7], i >> 1), sel);
-          mma_16816(oacc[i], a0, a1, a2, a3, ph[0], ph[1]);
-          mma_16816(oacc[i], a0, a1, a2, a3, pl[0], pl[1]);
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t x = __byte_perm(w[2 * h], 0u, 0x3120), y = __byte_perm(w[2 * h + 1], 0u, 0x3120);
+          const uint32_t a0 = e4m3x2_to_f16x2(x & 0xffffu), a1 = e4m3x2_to_f16x2(x >> 16);
+          const uint32_t a2 = e4m3x2_to_f16x2(y & 0xffffu), a3 = e4m3x2_to_f16x2(y >> 16);
+          mma_16816_f16(o, a0, a1, a2, a3, ph[2 * h], ph[2 * h + 1]);
+          mma_16816_f16(o, a0, a1, a2, a3, pl[2 * h], pl[2 * h + 1]);
         }
+      } else {
+        // Chunks 2i, 2i + 1 of keys 0-7, then of keys 8-15.
+        const int r = (mj >> 1) * 8 + l8;
+        ldsm_x4_t(vs + (uint32_t)(r * RB + (((2 * i + (mj & 1)) ^ l8) << 4)), w[0], w[1], w[2], w[3]);
+        mma_16816(o, w[0], w[1], w[2], w[3], ph[0], ph[1]);
+        mma_16816(o, w[0], w[1], w[2], w[3], pl[0], pl[1]);
       }
+      oacc[i][0] = fmaf(oacc[i][0], ca, o[0]);
+      oacc[i][1] = fmaf(oacc[i][1], cb, o[1]);
+      oacc[i][2] = fmaf(oacc[i][2], ca, o[2]);
+      oacc[i][3] = fmaf(oacc[i][3], cb, o[3]);
     }
-    if (more) load_v(row_next);
-    row = row_next;
+#pragma unroll
+    for (int i = 0; i < NS - 1; ++i) rq[i] = rq[i + 1];
+    st = st == NS - 1 ? 0 : st + 1;
   }
+  cp_async_wait<0>();
+  __syncthreads();  // every warp is done with its ring: mo and ml lie over them
 
   l_run += __shfl_xor_sync(kFull, l_run, 1);
   l_run += __shfl_xor_sync(kFull, l_run, 2);
@@ -428,7 +461,7 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
   float* mw = mo + (size_t)warp * kMaxGroup * kD;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int c0 = K8 ? 16 * gq + 2 * i : 8 * gq + i, c1 = K8 ? c0 + 1 : c0 + 64;
+    const int c0 = K8 ? 16 * i + 2 * gq : 16 * i + gq, c1 = K8 ? c0 + 1 : c0 + 8;
     mw[(2 * tq) * kD + c0] = oacc[i][0] * os * oe;
     mw[(2 * tq + 1) * kD + c0] = oacc[i][1] * os * oe;
     mw[(2 * tq) * kD + c1] = oacc[i][2] * os * oe;
@@ -438,6 +471,7 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
     ml[(warp * kMaxGroup + gq) * 2] = m_run;
     ml[(warp * kMaxGroup + gq) * 2 + 1] = l_run;
   }
+  __syncthreads();
 }
 
 // Writes output channel c of query head `head` (and, for c == 0, its log of the weights' sum).
@@ -452,7 +486,9 @@ __device__ __forceinline__ void put_out(const PageAttnArgs& a, size_t head, int 
     a.lse[head] = ((M == -INFINITY ? 0.f : M) + log2f(L)) * 0.6931471805599453f;
 }
 
-inline size_t page_attn_smem() { return (size_t)kPaWarps * kMaxGroup * (kD + 2) * 4; }
+// The rings; the warps' states lie over them.
+inline size_t page_attn_smem() { return (size_t)kPaWarps * kPaRing; }
+static_assert(kMaxGroup * (kD + 2) * 4 <= kPaRing, "a warp's state fits its ring");
 
 template <bool K8, bool kList>
 __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(PageAttnArgs a) {
@@ -461,26 +497,31 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
   float* mo = reinterpret_cast<float*>(pa_smem);
   float* ml = mo + kPaWarps * kMaxGroup * kD;
   const int tid = threadIdx.x, gs = a.Hq / a.Gs;
-  int total, b, off, c = blockIdx.x, n = a.n_ctas;
+  pdl_trigger();  // page_join_kernel waits for this grid's end before it reads the partials
+  int total, b, off, row, ub;  // row: over all sequences and tokens; ub: its units
+  const int c = blockIdx.x;
   if (kList) {
-    total = a.B * a.T * a.Gs * units_of(a.m_max * a.P);
+    ub = units_of(a.m_max * a.P);
+    total = a.B * a.T * a.Gs * ub;
   } else {
-    total = dense_scan(a, -1, sh, &b, &off);
+    const DensePlace p = dense_place(a, sh, [&](int all) {
+      return min(share_begin(c, all, min(a.n_ctas, all)), all - 1);
+    });
+    total = p.total;
+    b = p.b;
+    off = p.before;
   }
-  n = min(n, total);
+  const int n = min(a.n_ctas, total);
   if (c >= n) return;
   int u = share_begin(c, total, n);
   const int end = share_begin(c + 1, total, n);
-  if (!kList) dense_scan(a, u, sh, &b, &off);
-  int row = 0, ub;  // selection row (over all sequences and tokens), units of it
   if (kList) {
-    ub = units_of(a.m_max * a.P);
     row = u / ub;
     off = u - row * ub;
   } else {
     ub = units_of(dense_len(a, b));
-    row = b * a.Gs + off / ub;
-    off %= ub;
+    row = b * a.Gs + (u - off) / ub;
+    off = (u - off) % ub;
   }
   while (true) {
     const int take = min(end - u, ub - off);
@@ -516,8 +557,8 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
     __syncthreads();  // the new row is visible; the previous segment's state has been read
     const size_t head0 = (size_t)bt * a.Hq + (size_t)r * gs;
     page_segment<K8, kList>(a, rk, a.q + head0 * kD, gs, off * kUnitKeys,
-                            min(rk.n, (off + take) * kUnitKeys), mo, ml);
-    __syncthreads();
+                            min(rk.n, (off + take) * kUnitKeys),
+                            reinterpret_cast<char*>(pa_smem), mo, ml);
     const bool whole = off == 0 && take == ub;
     const size_t slot = 2 * (size_t)c + (off == 0 ? 1 : 0);
     for (int i = tid; i < gs * kD; i += kPaThreads) {
@@ -552,47 +593,83 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
       ub = units_of(dense_len(a, b));
     }
   }
-  pdl_trigger();
 }
 
-// Joins the partials of one row: the CTAs c0..c1 whose shares touch it, the first of them with
-// its "row begins here" slot, the others with their "row goes on" slot. One CTA per row; rows
-// that one CTA covered are already written.
-constexpr int kJoinThreads = 256;
+// Joins the partials of one row and head: the CTAs c0..c1 whose shares touch the row, the first
+// of them with its "row begins here" slot, the others with their "row goes on" slot. Grid (row,
+// head of the row); rows that one CTA covered are already written. The weights 2^(m - M) are
+// taken once per partial, by one thread each; then warp w sums the partials w, w + 8, ..., a lane
+// holding 4 channels, and the 8 sums are added in order.
+constexpr int kJoinWarps = 8;
+constexpr int kJoinThreads = kJoinWarps * 32;
+constexpr int kJoinChunk = kJoinThreads;  // partials whose weights are in shared memory at a time
 template <bool kList>
 __global__ void __launch_bounds__(kJoinThreads) page_join_kernel(PageAttnArgs a) {
   __shared__ int sh[40];
-  const int row = blockIdx.x, tid = threadIdx.x, gs = a.Hq / a.Gs;
-  int total, first, ub, b, off;
+  __shared__ float wt[kJoinChunk], red[2][kJoinWarps];
+  __shared__ __align__(16) float acc[kJoinWarps][kD];
+  const int row = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, gs = a.Hq / a.Gs;
+  const int lane = tid & 31, warp = tid >> 5;
+  int total, first, ub;
   if (kList) {
     ub = units_of(a.m_max * a.P);
     total = a.B * a.T * a.Gs * ub;
     first = row * ub;
   } else {
     const int bs = row / a.Gs;
-    total = dense_scan(a, -1 - bs, sh, &b, &off);
+    const DensePlace p = dense_place(a, sh, [&](int) { return -1 - bs; });
+    total = p.total;
     ub = units_of(dense_len(a, bs));
-    first = off + (row - bs * a.Gs) * ub;
+    first = p.before + (row - bs * a.Gs) * ub;
   }
   const int n = min(a.n_ctas, total);
-  const int c0 = share_of(first, total, n), c1 = share_of(first + ub - 1, total, n);
+  const int c0 = share_of(first, total, n), parts = share_of(first + ub - 1, total, n) - c0 + 1;
   pdl_wait();
-  if (c0 == c1) return;
-  const int bt = row / a.Gs, r = row - bt * a.Gs;
-  const size_t head0 = (size_t)bt * a.Hq + (size_t)r * gs;
-  for (int i = tid; i < gs * kD; i += kJoinThreads) {
-    const int h = i / kD, ch = i % kD;
-    auto slot = [&](int c) { return ((size_t)2 * c + (c == c0 ? 1 : 0)) * gs + h; };
-    float M = -INFINITY;
-    for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(a.part_ml + slot(c) * 2));
-    const float mu = M == -INFINITY ? 0.f : M;
-    float L = 0.f, O = 0.f;
-    for (int c = c0; c <= c1; ++c) {
-      const float f = exp2f(__ldcg(a.part_ml + slot(c) * 2) - mu);
-      L = fmaf(f, __ldcg(a.part_ml + slot(c) * 2 + 1), L);
-      O = fmaf(f, __ldcg(a.part_o + slot(c) * kD + ch), O);
+  if (parts == 1) return;
+  auto slot = [&](int i) { return ((size_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * gs + h; };
+  float M = -INFINITY;
+  for (int i = tid; i < parts; i += kJoinThreads) M = fmaxf(M, __ldcg(a.part_ml + slot(i) * 2));
+  M = warp_max(M);
+  if (lane == 0) red[0][warp] = M;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) M = fmaxf(M, red[0][w]);
+  const float mu = M == -INFINITY ? 0.f : M;
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < parts; i0 += kJoinChunk) {
+    if (i0 > 0) __syncthreads();
+    if (i0 + tid < parts) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(a.part_ml) + slot(i0 + tid));
+      wt[tid] = exp2f(ml.x - mu);
+      L = fmaf(wt[tid], ml.y, L);
     }
-    put_out(a, head0 + h, ch, M, L, O);
+    __syncthreads();
+    const int k = min(kJoinChunk, parts - i0);
+#pragma unroll 4
+    for (int i = warp; i < k; i += kJoinWarps) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot(i0 + i) * kD) + lane);
+      const float f = wt[i];
+      o.x = fmaf(f, v.x, o.x);
+      o.y = fmaf(f, v.y, o.y);
+      o.z = fmaf(f, v.z, o.z);
+      o.w = fmaf(f, v.w, o.w);
+    }
+  }
+  reinterpret_cast<float4*>(acc[warp])[lane] = o;
+  L = warp_sum(L);
+  if (lane == 0) red[1][warp] = L;
+  __syncthreads();
+  if (tid < kD) {
+    float O = 0.f;
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      O += acc[w][tid];
+      L += red[1][w];
+    }
+    const int bt = row / a.Gs, r = row - bt * a.Gs;
+    put_out(a, (size_t)bt * a.Hq + (size_t)r * gs + h, tid, M, L, O);
   }
 }
 

@@ -330,7 +330,7 @@ def _t(t, dtypes, name, n, dev):
 
 def _here(stream):
     """(current device, raw stream handle) of a call."""
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice()
     if stream is None:
         return dev, torch._C._cuda_getCurrentRawStream(dev)
     return dev, stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
