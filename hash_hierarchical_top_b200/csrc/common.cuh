@@ -216,6 +216,61 @@ __device__ __forceinline__ void hist_add_aggregated(int* hist, int bin, bool act
   if ((threadIdx.x & 31) == leader) atomicAdd(&hist[bin], __popc(peers));
 }
 
+// ---- Work of a ragged batch laid end to end and divided evenly ----
+// Worker c's share of `total` units over n CTAs: [c total / n, (c + 1) total / n). n <= total.
+__device__ __forceinline__ int share_begin(int c, int total, int n) {
+  return (int)((long long)c * total / n);
+}
+// The worker whose share holds unit u.
+__device__ __forceinline__ int share_of(int u, int total, int n) {
+  return (int)((((long long)u + 1) * n - 1) / total);
+}
+
+// Where a place of the batch's units lies: sequence b, `before` units ahead of it, and all the
+// units of the call.
+struct UnitPlace {
+  int total, b, before;
+};
+// Block-wide: B sequences of units(b) units each. pick(total) is the unit that is looked for
+// (>= 0, < total), or -1 - b for the place of sequence b. Up to 32 sequences every warp scans
+// them on its own, without a barrier; else the block does. sh: 40 ints.
+template <typename Units, typename Pick>
+__device__ __forceinline__ UnitPlace place_units(int B, int* sh, Units units, Pick pick) {
+  const int tid = threadIdx.x, lane = tid & 31;
+  UnitPlace r;
+  if (B <= 32) {
+    const int u = lane < B ? units(lane) : 0;
+    const int incl = warp_incl_scan(u, lane);
+    r.total = __shfl_sync(kFull, incl, 31);
+    const int want = pick(r.total);
+    // The first sequence whose units end behind the wanted one.
+    r.b = want >= 0 ? __ffs(__ballot_sync(kFull, incl > want)) - 1 : -1 - want;
+    r.before = __shfl_sync(kFull, incl - u, r.b);
+    return r;
+  }
+  const int per = (B + blockDim.x - 1) / blockDim.x;
+  const int b0 = min(B, tid * per), b1 = min(B, b0 + per);
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) sum += units(b);
+  int before = block_excl_scan(sum, sh, &r.total);
+  const int want = pick(r.total);
+  if (want >= 0 ? (want >= before && want < before + sum) : (-1 - want >= b0 && -1 - want < b1)) {
+    int b = b0;
+    while (true) {
+      const int u = units(b);
+      if (want >= 0 ? want < before + u : b == -1 - want) break;
+      before += u;
+      ++b;
+    }
+    sh[36] = b;
+    sh[37] = before;
+  }
+  __syncthreads();
+  r.b = sh[36];
+  r.before = sh[37];
+  return r;
+}
+
 // Order-preserving map of a float to uint32 (larger float -> larger key; -0 < +0).
 __device__ __forceinline__ uint32_t f2key(float f) {
   uint32_t u = __float_as_uint(f);

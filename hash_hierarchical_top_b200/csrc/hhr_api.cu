@@ -960,7 +960,7 @@ int hhr_read_device_status(void* stream, int* bits) {
 
 namespace {
 
-bool g_smem_page[2][2][kMaxDevices], g_smem_topm[kMaxDevices], g_smem_tile[kMaxDevices];
+bool g_smem_page[2][2][kMaxDevices], g_smem_cluster[2][2][kMaxDevices], g_smem_topm[2][kMaxDevices];
 
 // Cache rows are addressed with 32-bit row indices.
 bool rows_fit(const hhr_dims* d) {
@@ -976,6 +976,9 @@ int check_kv8(const hhr_dims* d, const uint8_t* k, const uint8_t* v, const uint8
   return rows_fit(d) ? HHR_OK : HHR_ERR_UNSUPPORTED;
 }
 
+#ifndef HHR_BS_NARROW
+#define HHR_BS_NARROW 1024
+#endif
 constexpr int kMaxListBlocks = 32768;  // blocks per list
 // Dynamic shared memory that needs no opt-in, beside a few KB of static shared memory.
 constexpr size_t kDefaultSmem = 36 * 1024;
@@ -995,6 +998,29 @@ size_t page_ws(const hhr_dims* d, int n_ctas) {
   return align256((size_t)2 * n_ctas * gs * kD * 4) + align256((size_t)2 * n_ctas * gs * 2 * 4);
 }
 
+// CTAs of the cluster that takes one row, or 0 for even shares of all rows' keys with a join.
+// Clusters need one launch and no join, but split every row alike: they are taken where all rows'
+// clusters are resident at once, for lists (rows of one capacity), and for dense rows of up to
+// HHR_PA_DENSE_CLUSTER keys (or of a single sequence up to HHR_PA_DENSE_CLUSTER1).
+#ifndef HHR_PA_DENSE_CLUSTER
+#define HHR_PA_DENSE_CLUSTER 2048
+#endif
+#ifndef HHR_PA_DENSE_CLUSTER1
+#define HHR_PA_DENSE_CLUSTER1 4096
+#endif
+#ifndef HHR_PA_LIST_CLUSTER
+#define HHR_PA_LIST_CLUSTER 1
+#endif
+int page_cluster(const hhr_dims* d, int T, int blocks, bool list) {
+  const long long rows = (long long)d->batch * T * sel_rows(d);
+  const long long keys = (long long)blocks * d->page_size, n = (long long)kPaCtasPerSm * sm_count();
+  if (rows > n || (list && !HHR_PA_LIST_CLUSTER)) return 0;
+  if (!list && keys > (d->batch == 1 ? HHR_PA_DENSE_CLUSTER1 : HHR_PA_DENSE_CLUSTER)) return 0;
+  int cs = kPaMaxCluster;
+  while (cs > 1 && (rows * cs > n || (long long)(cs / 2) * kUnitKeys >= keys)) cs /= 2;
+  return cs;
+}
+
 // Launches the page attention and, where CTAs can share a row, the join of its partials.
 template <bool kList>
 int launch_page_attn(const hhr_dims* d, PageAttnArgs& a, bool k8, long long units, void* workspace,
@@ -1002,12 +1028,37 @@ int launch_page_attn(const hhr_dims* d, PageAttnArgs& a, bool k8, long long unit
   a.B = d->batch; a.Hq = d->n_q_heads; a.G = d->n_kv_heads; a.Gs = sel_rows(d);
   a.kv_div = kv_div(d); a.P = d->page_size; a.maxp = d->max_pages_per_seq;
   a.n_phys = d->n_phys_pages;
+  a.n_rows = (uint32_t)a.n_phys * (uint32_t)a.G * (uint32_t)a.P;
   a.p_mul = (uint32_t)((0x100000000ull + (unsigned)a.P - 1) / (unsigned)a.P);
   a.n_ctas = page_ctas(units);
   const size_t gs = a.Hq / a.Gs;
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                        align256((size_t)2 * a.n_ctas * gs * kD * 4));
+  const int cs = page_cluster(d, a.T, kList ? a.m_max : a.maxp, kList);
+  if (cs > 0) {
+    void (*kc)(PageAttnArgs) =
+        k8 ? page_cluster_kernel<true, kList> : page_cluster_kernel<false, kList>;
+    if (allow_smem(kc, page_attn_smem(), g_smem_cluster[k8][kList]) != cudaSuccess)
+      return HHR_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.B * a.T * a.Gs * cs));
+    cfg.blockDim = dim3(kPaThreads);
+    cfg.dynamicSmemBytes = page_attn_smem();
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cs;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    prof_begin(HHR_KERNEL_PAGE, s);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kc, a);
+    prof_end(HHR_KERNEL_PAGE, s);
+    if (e != cudaSuccess) { g_last_cuda = e; return HHR_ERR_CUDA; }
+    return HHR_OK;
+  }
   void (*k)(PageAttnArgs) = k8 ? page_attn_kernel<true, kList> : page_attn_kernel<false, kList>;
   if (allow_smem(k, page_attn_smem(), g_smem_page[k8][kList]) != cudaSuccess) return HHR_ERR_CUDA;
   prof_begin(HHR_KERNEL_PAGE, s);
@@ -1046,6 +1097,9 @@ int check_chunk(const hhr_dims* d, int n_queries) {
   if (n_queries < 1) return HHR_ERR_INVALID_ARG;
   const long long rows = (long long)d->batch * n_queries * d->n_q_heads;
   return rows > 0x7fffffffLL ? HHR_ERR_UNSUPPORTED : HHR_OK;
+}
+size_t select_scores_bytes(const hhr_dims* d, int n_queries) {
+  return align256((size_t)d->batch * n_queries * sel_rows(d) * d->max_pages_per_seq * 4);
 }
 int check_dense(const hhr_dims* d) {
   int st = check_dims(d);
@@ -1148,7 +1202,8 @@ int hhr_paged_attn(const hhr_dims* d, const uint16_t* q, const uint16_t* k_new,
 
 size_t hhr_block_select_workspace_bytes(const hhr_dims* d, int n_queries) {
   if (check_chunk(d, n_queries) != HHR_OK) return 0;
-  return align256((size_t)d->batch * n_queries * sel_rows(d) * d->max_pages_per_seq * 4);
+  return select_scores_bytes(d, n_queries) +
+         align256((size_t)d->batch * d->n_kv_heads * d->max_pages_per_seq * 4);
 }
 
 int hhr_block_select(const hhr_dims* d, int n_queries, const uint16_t* q, const int32_t* seq_len,
@@ -1169,30 +1224,40 @@ int hhr_block_select(const hhr_dims* d, int n_queries, const uint16_t* q, const 
   cudaStream_t s = (cudaStream_t)stream;
   const int B = d->batch, Gs = sel_rows(d), maxp = d->max_pages_per_seq;
   BlockSelectArgs a{q, seq_len, q_pos, page_table, block_mean, static_cast<float*>(workspace),
+                    reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                             select_scores_bytes(d, n_queries)),
                     out_blocks, out_count, B, n_queries, d->n_q_heads, d->n_kv_heads, Gs,
                     kv_div(d), d->page_size, maxp, d->n_phys_pages, m_pages,
-                    kept_max(d, m_pages, 0), sink, local};
-  const size_t smem = (size_t)maxp * 4;
+                    kept_max(d, m_pages, 0), sink, local, 0};
+  const size_t smem = block_topm_smem(maxp);
   // Rows of one KV group, and their tiles over all groups.
   const long long rows = (long long)n_queries * a.kv_div;
   const long long tiles = (rows + kBtRows - 1) / kBtRows * d->n_kv_heads;
-  if (tiles > 65535) return HHR_ERR_UNSUPPORTED;
-  if (rows > 1 && allow_smem(block_mean_tile_kernel, block_tile_smem(), g_smem_tile) != cudaSuccess)
-    return HHR_ERR_CUDA;
-  if (smem > kDefaultSmem && allow_smem(block_topm_kernel, smem, g_smem_topm) != cudaSuccess)
+  if (tiles > 65535 || (long long)B * maxp > 0x7fffffffLL) return HHR_ERR_UNSUPPORTED;
+  // A single row per group is a stream over the means (20.5 us of bytes for 8 sequences of 4096
+  // blocks x 8 groups); more rows are a matrix product of tiles.
+  const bool single = rows == 1 && d->n_kv_heads <= kBvMaxGroups;
+  const long long stream_ctas = min(((long long)B * maxp * d->n_kv_heads + kBvItem - 1) / kBvItem,
+                                    (long long)kBvCtasPerSm * sm_count());
+  a.g_mul = (uint32_t)((0x100000000ull + (unsigned)a.G - 1) / (unsigned)a.G);
+  // The choice: few threads per row of up to 1024 blocks (bound by barriers; more rows fit an
+  // SM), more threads for longer rows.
+  const int wide = maxp > HHR_BS_NARROW;
+  void (*topm)(BlockSelectArgs) = wide ? block_topm_kernel<512> : block_topm_kernel<128>;
+  if (smem > kDefaultSmem && allow_smem(topm, smem, g_smem_topm[wide]) != cudaSuccess)
     return HHR_ERR_CUDA;
   prof_begin(HHR_KERNEL_MEAN, s);
-  if (rows == 1)
-    block_mean_stream_kernel<<<dim3((maxp + kBvWarps * 32 - 1) / (kBvWarps * 32), d->n_kv_heads, B),
-                               kBvWarps * 32, 0, s>>>(a);
+  if (single)
+    block_mean_stream_kernel<<<(unsigned)stream_ctas, kBvWarps * 32,
+                               block_stream_smem(d->n_kv_heads), s>>>(a);
   else
     block_mean_tile_kernel<<<dim3((maxp + kBtPages - 1) / kBtPages, (unsigned)tiles, B), kBtThreads,
                              block_tile_smem(), s>>>(a);
   prof_end(HHR_KERNEL_MEAN, s);
   if ((st = launch_status()) != HHR_OK) return st;
   prof_begin(HHR_KERNEL_TOPM, s);
-  const cudaError_t e = launch_pdl(block_topm_kernel, dim3((unsigned)(B * n_queries * Gs)),
-                                   dim3(kBsSelThreads), smem, s, a);
+  const cudaError_t e = launch_pdl(topm, dim3((unsigned)(B * n_queries * Gs)),
+                                   dim3(wide ? 512 : 128), smem, s, a);
   prof_end(HHR_KERNEL_TOPM, s);
   if (e != cudaSuccess) { g_last_cuda = e; return HHR_ERR_CUDA; }
   return HHR_OK;

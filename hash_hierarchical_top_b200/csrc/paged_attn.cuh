@@ -47,13 +47,13 @@ namespace hhr {
 #define HHR_PA_WARPS 4
 #endif
 #ifndef HHR_PA_CTAS
-#define HHR_PA_CTAS 2
+#define HHR_PA_CTAS 3
 #endif
 #ifndef HHR_PA_UNIT
 #define HHR_PA_UNIT 128
 #endif
 #ifndef HHR_PA_STAGES
-#define HHR_PA_STAGES 3
+#define HHR_PA_STAGES 2
 #endif
 constexpr int kPaStages = HHR_PA_STAGES;
 constexpr int kPaWarps = HHR_PA_WARPS;
@@ -83,6 +83,7 @@ struct PageAttnArgs {
   int B, T, Hq, G, Gs, kv_div, P, maxp, n_phys, m_max;
   uint32_t p_mul;              // ceil(2^32 / P): j / P = umulhi(j, p_mul) for P > 1
   int n_ctas;
+  uint32_t n_rows;             // n_phys G P
 };
 
 // j / P for 0 <= j < 2^24, P <= 256: the error of j p_mul / 2^32 is below j P / 2^32 < 1 / P.
@@ -98,60 +99,26 @@ __device__ __forceinline__ int units_of(int keys) {
   return max(1, (keys + kUnitKeys - 1) / kUnitKeys);
 }
 
-// CTA c's share of `total` units over n CTAs: [c total / n, (c + 1) total / n). n <= total.
-__device__ __forceinline__ int share_begin(int c, int total, int n) {
-  return (int)((long long)c * total / n);
-}
-// The CTA whose share holds unit u.
-__device__ __forceinline__ int share_of(int u, int total, int n) {
-  return (int)((((long long)u + 1) * n - 1) / total);
-}
-
-// Where a place of the dense rows' units lies: sequence b, `before` units ahead of it, and all
-// the units of the call.
-struct DensePlace {
-  int total, b, before;
-};
-// Block-wide: a.B sequences, each counted Gs times. pick(total) is the unit that is looked for
-// (>= 0), or -1 - b for the place of sequence b. Up to 32 sequences every warp scans them on its
-// own, without a barrier; else the block does. sh: 40 ints.
+// Units of sequence b, over its rows, and the place that `pick` asks for (UnitPlace).
 template <typename Pick>
-__device__ __forceinline__ DensePlace dense_place(const PageAttnArgs& a, int* sh, Pick pick) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  DensePlace r;
-  if (a.B <= 32) {
-    const int u = lane < a.B ? units_of(dense_len(a, lane)) * a.Gs : 0;
-    const int incl = warp_incl_scan(u, lane);
-    r.total = __shfl_sync(kFull, incl, 31);
-    const int want = pick(r.total);
-    // The first sequence whose units end behind the wanted one.
-    r.b = want >= 0 ? __ffs(__ballot_sync(kFull, incl > want)) - 1 : -1 - want;
-    r.before = __shfl_sync(kFull, incl - u, r.b);
-    return r;
-  }
-  const int per = (a.B + blockDim.x - 1) / blockDim.x;
-  const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  int sum = 0;
-  for (int b = b0; b < b1; ++b) sum += units_of(dense_len(a, b)) * a.Gs;
-  int before = block_excl_scan(sum, sh, &r.total);
-  const int want = pick(r.total);
-  if (want >= 0 ? (want >= before && want < before + sum) : (-1 - want >= b0 && -1 - want < b1)) {
-    int b = b0;
-    while (true) {
-      const int u = units_of(dense_len(a, b)) * a.Gs;
-      if (want >= 0 ? want < before + u : b == -1 - want) break;
-      before += u;
-      ++b;
-    }
-    sh[36] = b;
-    sh[37] = before;
-  }
-  __syncthreads();
-  r.b = sh[36];
-  r.before = sh[37];
-  return r;
+__device__ __forceinline__ UnitPlace dense_place(const PageAttnArgs& a, int* sh, Pick pick) {
+  return place_units(a.B, sh, [&](int b) { return units_of(dense_len(a, b)) * a.Gs; }, pick);
 }
 
+// 16 bytes into shared memory.
+__device__ __forceinline__ void cp_async16_at(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+// 4 bytes into shared memory, of which the first n are read and the others are zeros.
+__device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
 // 16 bytes into shared memory; n = 0 writes zeros and reads nothing.
 __device__ __forceinline__ void cp_async16_zfill(uint32_t dst, const void* src, uint32_t n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(n)
@@ -166,6 +133,12 @@ __device__ __forceinline__ void mma_16816_f16(float (&d)[4], uint32_t a0, uint32
       "{%8,%9}, {%0,%1,%2,%3};\n"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// 2^x to 2^-22 relative; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+  return r;
 }
 __device__ __forceinline__ uint32_t pack_f16(float x, float y) {
   const __half2 h = __floats2half2_rn(x, y);
@@ -194,40 +167,48 @@ struct RowKeys {
   uint32_t g;             // KV head
 };
 
-// The page id that slot j needs (list: through the block list), or a negative number with the
-// status word set; -1 alone when the slot holds no key.
+// Locating a key takes three steps, each of which uses what the one before it loaded. The loop
+// runs them one iteration apart and leaves a loaded value alone until the next iteration (a use
+// at once would stall the warp for the load's latency in every step).
+constexpr int kNoKey = (int)0x80000000;  // a slot that holds no key
+// The block of slot j: dense, its page; list, the entry as it is listed.
 template <bool kList>
-__device__ __forceinline__ int block_of(const PageAttnArgs& a, const RowKeys& r, int j) {
-  if (j >= r.n) return -1;
-  if (!kList) return page_of(a, j);
-  const int p = r.blocks[page_of(a, j)];
-  if (p < 0 || p >= a.maxp) {
+__device__ __forceinline__ int load_block(const PageAttnArgs& a, const RowKeys& r, int j, int k1) {
+  if (j >= k1) return kNoKey;
+  return kList ? r.blocks[page_of(a, j)] : page_of(a, j);
+}
+// The page-table entry of a loaded block, and kNoKey where it is not a block with keys.
+template <bool kList>
+__device__ __forceinline__ int load_page(const PageAttnArgs& a, const RowKeys& r, int& block) {
+  if (kList && block != kNoKey && (block < 0 || block >= a.maxp)) {
     flag_status(kStatusBadToken);
-    return -1;
+    block = kNoKey;
   }
-  return p;
+  if (block == kNoKey || block * a.P >= r.limit) return kNoKey;
+  return r.pages[block];
 }
-__device__ __forceinline__ int phys_of(const PageAttnArgs& a, const RowKeys& r, int block) {
-  if (block < 0 || block * a.P >= r.limit) return -1;
-  const int phys = r.pages[block];
-  if (phys < 0 || phys >= a.n_phys) {
-    flag_status(kStatusBadPage);
-    return -1;
-  }
-  return phys;
-}
+// The cache row of slot j, or kNoRow.
 __device__ __forceinline__ uint32_t row_of(const PageAttnArgs& a, const RowKeys& r, int j,
-                                           int block, int phys) {
+                                           int block, int page) {
+  if (page == kNoKey) return kNoRow;
+  if (page < 0 || page >= a.n_phys) {
+    flag_status(kStatusBadPage);
+    return kNoRow;
+  }
   const int slot = j - page_of(a, j) * a.P;
-  if (phys < 0 || block * a.P + slot >= r.limit) return kNoRow;
-  return ((uint32_t)phys * (uint32_t)a.G + r.g) * (uint32_t)a.P + (uint32_t)slot;
+  if (block * a.P + slot >= r.limit) return kNoRow;
+  return ((uint32_t)page * (uint32_t)a.G + r.g) * (uint32_t)a.P + (uint32_t)slot;
 }
 
 // Shared memory of one warp: kPaStages stages of a K tile and a V tile, S rows each (16 bf16 or
 // 32 8-bit rows: 4 KB a tile). The 16-byte chunks of a row are XOR-swizzled by row % 8, so that
 // ldmatrix reads of 8 rows hit 8 distinct bank groups.
+// Beside the tiles lie, for an 8-bit cache, the aligned words that hold the rows' exponent bytes
+// (32 of K, 32 of V): fetched like the rows, since their DRAM latency under load is longer than a
+// step.
 constexpr int kPaTile = 4096;
-constexpr int kPaRing = kPaStages * 2 * kPaTile;
+constexpr int kPaStage = 2 * kPaTile + 256;
+constexpr int kPaRing = kPaStages * kPaStage;
 
 // Keys [k0, k1) of a row, over the CTA's warps: the state of every head is left in shared
 // memory (mo [warps][8][d], ml [warps][8][2], which reuse the rings). Ends with the state of
@@ -249,60 +230,74 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
   const int base = k0 + warp * S, stride = kPaWarps * S;
   const int lk = K8 ? lane : (lane & 15);  // the key of a step that this lane locates
 
-  auto block_at = [&](int j) { return j < k1 ? block_of<kList>(a, rk, j) : -1; };
   // Copies the rows of a step (`row`: this lane's) into stage st; missing rows become zeros.
+  const char* kl = kb + 16 * (lane % RC);
+  const char* vl = vb + 16 * (lane % RC);
   auto issue = [&](uint32_t row, int st) {
-    const uint32_t ks = ring + (uint32_t)st * 2 * kPaTile;
+    const uint32_t ks = ring + (uint32_t)st * kPaStage;
+    if constexpr (K8) {
+      const uint32_t word = row & ~3u, n = row != kNoRow ? min(4u, a.n_rows - word) : 0u;
+      const uint32_t dst = ks + 2 * kPaTile + 4 * lane;
+      cp_async4_zfill(dst, a.k_exp + (n != 0u ? word : 0u), n);
+      cp_async4_zfill(dst + 128, a.v_exp + (n != 0u ? word : 0u), n);
+    }
+    if (__all_sync(kFull, row != kNoRow)) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = i * (32 / RC) + lane / RC, c = lane % RC;
-      const uint32_t o = __shfl_sync(kFull, row, r);
-      const uint32_t n = o != kNoRow ? 16u : 0u;
-      const size_t off = o != kNoRow ? (size_t)o * RB + 16 * c : 0;
-      const uint32_t dst = ks + (uint32_t)(r * RB + ((c ^ (r & 7)) << 4));
-      cp_async16_zfill(dst, kb + off, n);
-      cp_async16_zfill(dst + kPaTile, vb + off, n);
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * (32 / RC) + lane / RC, c = lane % RC;
+        const uint32_t o = __shfl_sync(kFull, row, r);
+        const uint32_t dst = ks + (uint32_t)(r * RB + ((c ^ (r & 7)) << 4));
+        cp_async16_at(dst, kl + (size_t)o * RB);
+        cp_async16_at(dst + kPaTile, vl + (size_t)o * RB);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * (32 / RC) + lane / RC, c = lane % RC;
+        const uint32_t o = __shfl_sync(kFull, row, r);
+        const uint32_t dst = ks + (uint32_t)(r * RB + ((c ^ (r & 7)) << 4));
+        const uint32_t n = o != kNoRow ? 16u : 0u;
+        const size_t off = o != kNoRow ? (size_t)o * RB : 0;
+        cp_async16_zfill(dst, kl + off, n);
+        cp_async16_zfill(dst + kPaTile, vl + off, n);
+      }
     }
   };
 
-  // rq[i]: the row this lane locates in step i from now. Page ids are loaded one step before
-  // the row index is needed, block ids one step before that.
+  // rq[i]: the row this lane locates in step i from now.
   uint32_t rq[NS];
-  int j0 = base + lk, blk1, phys1, blk2;
+  int j0 = base + lk, blk1, page1, blk2;
   {
-    int bl[NS + 1], ph[NS];
+    int bl[NS + 1], pg[NS];
 #pragma unroll
-    for (int i = 0; i <= NS; ++i) bl[i] = block_at(j0 + i * stride);
+    for (int i = 0; i <= NS; ++i) bl[i] = load_block<kList>(a, rk, j0 + i * stride, k1);
 #pragma unroll
-    for (int i = 0; i < NS; ++i) ph[i] = phys_of(a, rk, bl[i]);
+    for (int i = 0; i < NS; ++i) pg[i] = load_page<kList>(a, rk, bl[i]);
 #pragma unroll
     for (int i = 0; i < NS - 1; ++i) {
-      rq[i] = row_of(a, rk, j0 + i * stride, bl[i], ph[i]);
+      rq[i] = row_of(a, rk, j0 + i * stride, bl[i], pg[i]);
       issue(rq[i], i);
       cp_async_commit();
     }
     blk1 = bl[NS - 1];
-    phys1 = ph[NS - 1];
+    page1 = pg[NS - 1];
     blk2 = bl[NS];
     j0 += (NS - 1) * stride;
   }
-  // 8-bit: the exponent bytes of the row that this lane locates (K low, V next).
-  auto exponents = [&](uint32_t row) {
-    return row != kNoRow ? (uint32_t)a.k_exp[row] | (uint32_t)a.v_exp[row] << 8 : 0u;
-  };
-  uint32_t ex = K8 ? exponents(rq[0]) : 0u;
-
   // Query fragments (rows >= gs zero). bf16: MMA i takes the channels 16i..16i+15 in order;
   // 8-bit: k = 2tq, 2tq + 1, 2tq + 8, 2tq + 9 are the channels 16i + 4tq + {0, 1, 2, 3}.
+  // A negative scale goes into the queries' signs, so that the largest product is the largest
+  // logit: logit = hs * product in log2 units, hs > 0 (a scale of 0 becomes the smallest number).
   uint32_t qa[8][2];
-  float hs = a.scale_log2;
+  float hs = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
   {
     const bool hv = gq < gs;
+    const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
     const uint32_t* q2 = reinterpret_cast<const uint32_t*>(q + (size_t)(hv ? gq : 0) * kD);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      qa[i][0] = hv ? q2[8 * i + (K8 ? 2 * tq : tq)] : 0u;
-      qa[i][1] = hv ? q2[8 * i + (K8 ? 2 * tq + 1 : tq + 4)] : 0u;
+      qa[i][0] = hv ? q2[8 * i + (K8 ? 2 * tq : tq)] ^ sign : 0u;
+      qa[i][1] = hv ? q2[8 * i + (K8 ? 2 * tq + 1 : tq + 4)] ^ sign : 0u;
     }
     if constexpr (K8) {
       uint32_t top = 0u;
@@ -314,7 +309,7 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
       top = max(top, __shfl_xor_sync(kFull, top, 2));
       const uint32_t E = max(top >> 7, 15u);               // exponent field of the largest channel
       const float up = __uint_as_float((268u - E) << 23);  // 2^(14 - (E - 127))
-      hs = a.scale_log2 * __uint_as_float((E - 14u) << 23);
+      hs = fmaxf(hs * __uint_as_float((E - 14u) << 23), 1.17549435e-38f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         qa[i][0] = pack_f16(bf16_lo(qa[i][0]) * up, bf16_hi(qa[i][0]) * up);
@@ -335,13 +330,20 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
     cp_async_wait<NS - 2>();
     __syncwarp();  // the stage's rows are there; the previous step's stage has been read
     // The rows of NS - 1 steps ahead, and the page ids of the step after it.
-    rq[NS - 1] = row_of(a, rk, j0, blk1, phys1);
+    rq[NS - 1] = row_of(a, rk, j0, blk1, page1);
     issue(rq[NS - 1], st == 0 ? NS - 1 : st - 1);
     cp_async_commit();
     blk1 = blk2;
-    phys1 = phys_of(a, rk, blk1);
-    blk2 = block_at(j0 + 2 * stride);
-    const uint32_t ks = ring + (uint32_t)st * 2 * kPaTile, vs = ks + kPaTile;
+    page1 = load_page<kList>(a, rk, blk1);
+    blk2 = load_block<kList>(a, rk, j0 + 2 * stride, k1);
+    const uint32_t ks = ring + (uint32_t)st * kPaStage, vs = ks + kPaTile;
+    // 8-bit: the exponent bytes of the row that this lane located (K, V); 0 for none.
+    uint32_t xk = 0u, xv = 0u;
+    if constexpr (K8) {
+      const uint32_t at = ks + 2 * kPaTile + 4 * lane, sh = 8u * (rq[0] & 3u);
+      xk = (lds_u32(at) >> sh) & 0xffu;
+      xv = (lds_u32(at + 128) >> sh) & 0xffu;
+    }
     const unsigned ok = __ballot_sync(kFull, rq[0] != kNoRow);
 
     float sacc[NT][4];
@@ -357,8 +359,11 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
         if constexpr (K8) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            mma_16816_f16((i & 1) ? s2 : sacc[j], qa[c + i][0], 0u, qa[c + i][1], 0u,
-                          e4m3x2_to_f16x2(w[i] & 0xffffu), e4m3x2_to_f16x2(w[i] >> 16));
+          {
+            uint32_t b0, b1;
+            e4m3x4_to_f16x2(w[i], b0, b1);
+            mma_16816_f16((i & 1) ? s2 : sacc[j], qa[c + i][0], 0u, qa[c + i][1], 0u, b0, b1);
+          }
         } else {
           mma_16816(sacc[j], qa[c / 2][0], 0u, qa[c / 2][1], 0u, w[0], w[1]);
           mma_16816(s2, qa[c / 2 + 1][0], 0u, qa[c / 2 + 1][1], 0u, w[2], w[3]);
@@ -368,50 +373,55 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
       sacc[j][1] += s2[1];
     }
 
-    // Logits in log2 units, of head gq and the keys 8j + 2tq, 8j + 2tq + 1.
-    float mx = -INFINITY;
+    // Products of head gq and the keys 8j + 2tq, 8j + 2tq + 1. 8-bit: the lane that located a
+    // key hands out 2^k_exp and what its value's weight is scaled by, as two bf16 numbers.
     uint32_t e2[NT][2];
+    uint32_t e_new = e_run;
+    if constexpr (K8) {
+      e_new = max(e_run, __reduce_max_sync(kFull, xv));
+      const uint32_t mine = xk << 23 | (uint32_t)max(127 + 14 + (int)xv - (int)e_new, 0) << 7;
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int key = 8 * j + 2 * tq + i;
-        float sc = hs;
-        if constexpr (K8) {
-          e2[j][i] = __shfl_sync(kFull, ex, key);
-          sc *= exp_scale(e2[j][i] & 0xffu);
+        for (int i = 0; i < 2; ++i) {
+          e2[j][i] = __shfl_sync(kFull, mine, 8 * j + 2 * tq + i);
+          sacc[j][i] *= __uint_as_float(e2[j][i] & 0xffff0000u);
         }
-        sacc[j][i] = (ok >> key & 1u) ? sacc[j][i] * sc : -INFINITY;
-        mx = fmaxf(mx, sacc[j][i]);
-      }
     }
+    if (ok != kFull) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          if (!(ok >> (8 * j + 2 * tq + i) & 1u)) sacc[j][i] = -INFINITY;
+    }
+    float mx = fmaxf(sacc[0][0], sacc[0][1]);
+#pragma unroll
+    for (int j = 1; j < NT; ++j) mx = fmaxf(mx, fmaxf(sacc[j][0], sacc[j][1]));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
     const float m_new = fmaxf(m_run, mx);
     // What the sums so far are scaled by: head gq's, and those of the columns 2tq, 2tq + 1.
-    const float corr = m_new > m_run ? exp2f(m_run - m_new) : 1.f;
+    const float corr = m_new > m_run ? ex2((m_run - m_new) * hs) : 1.f;
     l_run *= corr;
     float ca = __shfl_sync(kFull, corr, 8 * tq), cb = __shfl_sync(kFull, corr, 8 * tq + 4);
     if constexpr (K8) {
-      const uint32_t e_new = max(e_run, __reduce_max_sync(kFull, ex >> 8));
       const float ec = exp_scale((uint32_t)max(127 + (int)e_run - (int)e_new, 0));
       ca *= ec;
       cb *= ec;
       e_run = e_new;
-      ex = exponents(rq[1]);
     }
     m_run = m_new;
-    const float mu = m_run == -INFINITY ? 0.f : m_run;
+    const float mu = m_run == -INFINITY ? 0.f : -m_run * hs;
     uint32_t ph[NT], pl[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       float p[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        p[i] = exp2f(sacc[j][i] - mu);
+        p[i] = ex2(fmaf(sacc[j][i], hs, mu));
         l_run += p[i];
-        if constexpr (K8)
-          p[i] *= exp_scale((uint32_t)max(127 + 14 + (int)(e2[j][i] >> 8) - (int)e_run, 0));
+        if constexpr (K8) p[i] *= __uint_as_float(e2[j][i] << 16);
       }
       split_pair<K8>(p[0], p[1], ph[j], pl[j]);
     }
@@ -428,9 +438,9 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
         ldsm_x4_t(vs + (uint32_t)(lane * RB + ((i ^ l8) << 4)), w[0], w[1], w[2], w[3]);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t x = __byte_perm(w[2 * h], 0u, 0x3120), y = __byte_perm(w[2 * h + 1], 0u, 0x3120);
-          const uint32_t a0 = e4m3x2_to_f16x2(x & 0xffffu), a1 = e4m3x2_to_f16x2(x >> 16);
-          const uint32_t a2 = e4m3x2_to_f16x2(y & 0xffffu), a3 = e4m3x2_to_f16x2(y >> 16);
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x2(__byte_perm(w[2 * h], 0u, 0x3120), a0, a1);
+          e4m3x4_to_f16x2(__byte_perm(w[2 * h + 1], 0u, 0x3120), a2, a3);
           mma_16816_f16(o, a0, a1, a2, a3, ph[2 * h], ph[2 * h + 1]);
           mma_16816_f16(o, a0, a1, a2, a3, pl[2 * h], pl[2 * h + 1]);
         }
@@ -468,7 +478,7 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
     mw[(2 * tq + 1) * kD + c1] = oacc[i][3] * os * oe;
   }
   if (tq == 0) {
-    ml[(warp * kMaxGroup + gq) * 2] = m_run;
+    ml[(warp * kMaxGroup + gq) * 2] = m_run * hs;  // in log2 units
     ml[(warp * kMaxGroup + gq) * 2 + 1] = l_run;
   }
   __syncthreads();
@@ -487,9 +497,65 @@ __device__ __forceinline__ void put_out(const PageAttnArgs& a, size_t head, int 
 }
 
 // The rings; the warps' states lie over them.
+constexpr int kPaMaxCluster = 8;
 inline size_t page_attn_smem() { return (size_t)kPaWarps * kPaRing; }
-static_assert(kMaxGroup * (kD + 2) * 4 <= kPaRing, "a warp's state fits its ring");
+static_assert((kPaWarps + 1) * kMaxGroup * (kD + 2) * 4 <= kPaWarps * kPaRing,
+              "the warps' states and the CTA's fit the rings");
 
+// Row `row` (over all sequences and tokens), sequence b: where its keys are.
+template <bool kList>
+__device__ __forceinline__ RowKeys row_keys(const PageAttnArgs& a, int row, int b) {
+  const int bt = row / a.Gs, r = row - bt * a.Gs;
+  RowKeys rk;
+  rk.pages = a.page_table + (size_t)b * a.maxp;
+  rk.g = (uint32_t)(a.kv_div == 1 ? r : r / a.kv_div);
+  rk.limit = dense_len(a, b);
+  if (kList && a.q_pos != nullptr) rk.limit = min(rk.limit - 1, a.q_pos[bt]) + 1;
+  rk.blocks = kList ? a.blocks + (size_t)row * a.m_max : nullptr;
+  rk.n = kList ? min(max(a.block_count[row], 0), a.m_max) * a.P : rk.limit;
+  if (!kList && threadIdx.x == 0 && a.seq_len[b] > a.maxp * a.P) flag_status(kStatusBadToken);
+  return rk;
+}
+
+// Dense: writes the newest row (position rk.n - 1) of sequence b into the cache; by the CTA that
+// reads it, before the barrier behind which it does.
+template <bool K8>
+__device__ __forceinline__ void append_row(const PageAttnArgs& a, const RowKeys& rk, int b) {
+  const int tid = threadIdx.x, t = rk.n - 1, l16 = tid & 15;
+  if (tid >= 32) return;
+  int lp = page_of(a, t);
+  const int page = load_page<false>(a, rk, lp);
+  const uint32_t o = row_of(a, rk, t, lp, page);
+  if (o == kNoRow) return;
+  const uint16_t* src = (tid < 16 ? a.k_new : a.v_new) + ((size_t)b * a.G + rk.g) * kD;
+  char* dst = reinterpret_cast<char*>(tid < 16 ? a.k : a.v);
+  const uint4 w = reinterpret_cast<const uint4*>(src)[l16];
+  if constexpr (K8) {
+    const uint32_t x = row_exponent(row_top16(w, 0xffffu << (tid & 16)));
+    *reinterpret_cast<uint2*>(dst + (size_t)o * kD + 8 * l16) = quantise8(w, x);
+    if (l16 == 0) (tid < 16 ? a.k_exp : a.v_exp)[o] = (uint8_t)x;
+  } else {
+    *reinterpret_cast<uint4*>(dst + (size_t)o * 2 * kD + 16 * l16) = w;
+  }
+}
+
+// Joins the warps' states of head h, channel ch.
+__device__ __forceinline__ void join_warps(const float* mo, const float* ml, int h, int ch, float& M,
+                                           float& L, float& O) {
+  M = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kPaWarps; ++w) M = fmaxf(M, ml[(w * kMaxGroup + h) * 2]);
+  const float mu = M == -INFINITY ? 0.f : M;
+  L = O = 0.f;
+#pragma unroll
+  for (int w = 0; w < kPaWarps; ++w) {
+    const float f = exp2f(ml[(w * kMaxGroup + h) * 2] - mu);
+    L = fmaf(f, ml[(w * kMaxGroup + h) * 2 + 1], L);
+    O = fmaf(f, mo[((size_t)w * kMaxGroup + h) * kD + ch], O);
+  }
+}
+
+// Even shares of all rows' keys (see the head of this file).
 template <bool K8, bool kList>
 __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(PageAttnArgs a) {
   extern __shared__ float4 pa_smem[];
@@ -504,7 +570,7 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
     ub = units_of(a.m_max * a.P);
     total = a.B * a.T * a.Gs * ub;
   } else {
-    const DensePlace p = dense_place(a, sh, [&](int all) {
+    const UnitPlace p = dense_place(a, sh, [&](int all) {
       return min(share_begin(c, all, min(a.n_ctas, all)), all - 1);
     });
     total = p.total;
@@ -527,33 +593,8 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
     const int take = min(end - u, ub - off);
     const int bt = row / a.Gs, r = row - bt * a.Gs;
     if (kList) b = bt / a.T;
-    RowKeys rk;
-    rk.pages = a.page_table + (size_t)b * a.maxp;
-    rk.g = (uint32_t)(a.kv_div == 1 ? r : r / a.kv_div);
-    rk.limit = dense_len(a, b);
-    if (a.q_pos != nullptr) rk.limit = min(rk.limit - 1, a.q_pos[bt]) + 1;
-    rk.blocks = kList ? a.blocks + (size_t)row * a.m_max : nullptr;
-    rk.n = kList ? min(max(a.block_count[row], 0), a.m_max) * a.P : rk.limit;
-    if (!kList && tid == 0 && a.seq_len[b] > a.maxp * a.P) flag_status(kStatusBadToken);
-    if (!kList && a.k_new != nullptr && off + take == ub && rk.n > 0) {
-      // The newest row lies in this segment: it is written before any of it is read.
-      const int t = rk.n - 1, lp = page_of(a, t);
-      const int phys = phys_of(a, rk, lp);
-      if (tid < 32 && phys >= 0) {
-        const int l16 = tid & 15;
-        const uint32_t o = row_of(a, rk, t, lp, phys);
-        const uint16_t* src = (tid < 16 ? a.k_new : a.v_new) + ((size_t)b * a.G + rk.g) * kD;
-        char* dst = reinterpret_cast<char*>(tid < 16 ? a.k : a.v);
-        const uint4 w = reinterpret_cast<const uint4*>(src)[l16];
-        if constexpr (K8) {
-          const uint32_t x = row_exponent(row_top16(w, 0xffffu << (tid & 16)));
-          *reinterpret_cast<uint2*>(dst + (size_t)o * kD + 8 * l16) = quantise8(w, x);
-          if (l16 == 0) (tid < 16 ? a.k_exp : a.v_exp)[o] = (uint8_t)x;
-        } else {
-          *reinterpret_cast<uint4*>(dst + (size_t)o * 2 * kD + 16 * l16) = w;
-        }
-      }
-    }
+    const RowKeys rk = row_keys<kList>(a, row, b);
+    if (!kList && a.k_new != nullptr && off + take == ub && rk.n > 0) append_row<K8>(a, rk, b);
     __syncthreads();  // the new row is visible; the previous segment's state has been read
     const size_t head0 = (size_t)bt * a.Hq + (size_t)r * gs;
     page_segment<K8, kList>(a, rk, a.q + head0 * kD, gs, off * kUnitKeys,
@@ -563,17 +604,8 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
     const size_t slot = 2 * (size_t)c + (off == 0 ? 1 : 0);
     for (int i = tid; i < gs * kD; i += kPaThreads) {
       const int h = i / kD, ch = i % kD;
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kPaWarps; ++w) M = fmaxf(M, ml[(w * kMaxGroup + h) * 2]);
-      const float mu = M == -INFINITY ? 0.f : M;
-      float L = 0.f, O = 0.f;
-#pragma unroll
-      for (int w = 0; w < kPaWarps; ++w) {
-        const float f = exp2f(ml[(w * kMaxGroup + h) * 2] - mu);
-        L = fmaf(f, ml[(w * kMaxGroup + h) * 2 + 1], L);
-        O = fmaf(f, mo[((size_t)w * kMaxGroup + h) * kD + ch], O);
-      }
+      float M, L, O;
+      join_warps(mo, ml, h, ch, M, L, O);
       if (whole) {
         put_out(a, head0 + h, ch, M, L, O);
       } else {
@@ -593,6 +625,67 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
       ub = units_of(dense_len(a, b));
     }
   }
+}
+
+// One cluster per row: its CTAs take equal parts of the row's keys and are joined through
+// distributed shared memory, each rank writing its share of the row's outputs. One launch, and no
+// partials in global memory.
+template <bool K8, bool kList>
+__global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_cluster_kernel(PageAttnArgs a) {
+  namespace cg = cooperative_groups;
+  extern __shared__ float4 pa_smem[];
+  float* mo = reinterpret_cast<float*>(pa_smem);
+  float* ml = mo + kPaWarps * kMaxGroup * kD;
+  float* res = ml + kPaWarps * kMaxGroup * 2;  // this CTA's state: [gs][d], then [gs][2]
+  cg::cluster_group cl = cg::this_cluster();
+  const int tid = threadIdx.x, gs = a.Hq / a.Gs;
+  const int cs = (int)cl.num_blocks(), rank = (int)cl.block_rank(), row = blockIdx.x / cs;
+  const int bt = row / a.Gs, r = row - bt * a.Gs, b = bt / a.T;
+  const RowKeys rk = row_keys<kList>(a, row, b);
+  constexpr int kIter = kPaWarps * (K8 ? 32 : 16);  // keys of an iteration of the CTA
+  const int per = ceil_div(ceil_div(rk.n, cs), kIter) * kIter;
+  const int k0 = min(rk.n, rank * per), k1 = min(rk.n, k0 + per);
+  if (!kList && a.k_new != nullptr && k0 < k1 && k1 == rk.n) append_row<K8>(a, rk, b);
+  __syncthreads();
+  const size_t head0 = (size_t)bt * a.Hq + (size_t)r * gs;
+  page_segment<K8, kList>(a, rk, a.q + head0 * kD, gs, k0, k1, reinterpret_cast<char*>(pa_smem), mo,
+                          ml);
+  for (int i = tid; i < gs * kD; i += kPaThreads) {
+    const int h = i / kD, ch = i % kD;
+    float M, L, O;
+    join_warps(mo, ml, h, ch, M, L, O);
+    res[h * kD + ch] = O;
+    if (ch == 0) {
+      res[kMaxGroup * kD + 2 * h] = M;
+      res[kMaxGroup * kD + 2 * h + 1] = L;
+    }
+  }
+  cluster_sync_all();  // every rank's state is in its shared memory
+  const int part = ceil_div(gs * kD, cs), i0 = rank * part, i1 = min(gs * kD, i0 + part);
+  for (int i = i0 + tid; i < i1; i += kPaThreads) {
+    const int h = i / kD, ch = i % kD;
+    float m[kPaMaxCluster], l[kPaMaxCluster], o[kPaMaxCluster];
+#pragma unroll
+    for (int c = 0; c < kPaMaxCluster; ++c) {
+      const float* x = cl.map_shared_rank(res, c < cs ? c : 0);
+      m[c] = c < cs ? x[kMaxGroup * kD + 2 * h] : -INFINITY;
+      l[c] = c < cs ? x[kMaxGroup * kD + 2 * h + 1] : 0.f;
+      o[c] = c < cs ? x[h * kD + ch] : 0.f;
+    }
+    float M = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < kPaMaxCluster; ++c) M = fmaxf(M, m[c]);
+    const float mu = M == -INFINITY ? 0.f : M;
+    float L = 0.f, O = 0.f;
+#pragma unroll
+    for (int c = 0; c < kPaMaxCluster; ++c) {
+      const float f = exp2f(m[c] - mu);
+      L = fmaf(f, l[c], L);
+      O = fmaf(f, o[c], O);
+    }
+    put_out(a, head0 + h, ch, M, L, O);
+  }
+  cluster_sync_all();  // no CTA leaves while its shared memory is read
 }
 
 // Joins the partials of one row and head: the CTAs c0..c1 whose shares touch the row, the first
@@ -617,7 +710,7 @@ __global__ void __launch_bounds__(kJoinThreads) page_join_kernel(PageAttnArgs a)
     first = row * ub;
   } else {
     const int bs = row / a.Gs;
-    const DensePlace p = dense_place(a, sh, [&](int) { return -1 - bs; });
+    const UnitPlace p = dense_place(a, sh, [&](int) { return -1 - bs; });
     total = p.total;
     ub = units_of(dense_len(a, bs));
     first = p.before + (row - bs * a.Gs) * ub;
