@@ -960,7 +960,8 @@ int hhr_read_device_status(void* stream, int* bits) {
 
 namespace {
 
-bool g_smem_page[2][2][kMaxDevices], g_smem_cluster[2][2][kMaxDevices], g_smem_topm[2][kMaxDevices];
+bool g_smem_page[2][2][2][kMaxDevices],
+    g_smem_cluster[2][2][2][kMaxDevices], g_smem_topm[2][kMaxDevices];
 
 // Cache rows are addressed with 32-bit row indices.
 bool rows_fit(const hhr_dims* d) {
@@ -1035,11 +1036,13 @@ int launch_page_attn(const hhr_dims* d, PageAttnArgs& a, bool k8, long long unit
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                        align256((size_t)2 * a.n_ctas * gs * kD * 4));
+  const bool pair = gs <= 4;  // both parts of the weights fit the 8 columns of one product
   const int cs = page_cluster(d, a.T, kList ? a.m_max : a.maxp, kList);
   if (cs > 0) {
     void (*kc)(PageAttnArgs) =
-        k8 ? page_cluster_kernel<true, kList> : page_cluster_kernel<false, kList>;
-    if (allow_smem(kc, page_attn_smem(), g_smem_cluster[k8][kList]) != cudaSuccess)
+        k8 ? (pair ? page_cluster_kernel<true, kList, true> : page_cluster_kernel<true, kList, false>)
+           : (pair ? page_cluster_kernel<false, kList, true> : page_cluster_kernel<false, kList, false>);
+    if (allow_smem(kc, page_attn_smem(), g_smem_cluster[k8][kList][pair]) != cudaSuccess)
       return HHR_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.B * a.T * a.Gs * cs));
@@ -1059,8 +1062,10 @@ int launch_page_attn(const hhr_dims* d, PageAttnArgs& a, bool k8, long long unit
     if (e != cudaSuccess) { g_last_cuda = e; return HHR_ERR_CUDA; }
     return HHR_OK;
   }
-  void (*k)(PageAttnArgs) = k8 ? page_attn_kernel<true, kList> : page_attn_kernel<false, kList>;
-  if (allow_smem(k, page_attn_smem(), g_smem_page[k8][kList]) != cudaSuccess) return HHR_ERR_CUDA;
+  void (*k)(PageAttnArgs) =
+      k8 ? (pair ? page_attn_kernel<true, kList, true> : page_attn_kernel<true, kList, false>)
+         : (pair ? page_attn_kernel<false, kList, true> : page_attn_kernel<false, kList, false>);
+  if (allow_smem(k, page_attn_smem(), g_smem_page[k8][kList][pair]) != cudaSuccess) return HHR_ERR_CUDA;
   prof_begin(HHR_KERNEL_PAGE, s);
   k<<<a.n_ctas, kPaThreads, page_attn_smem(), s>>>(a);
   prof_end(HHR_KERNEL_PAGE, s);

@@ -18,9 +18,8 @@
 //     pieces t, t + 4, ... of key g and the query fragments follow that order; in O^T = V^T P^T
 //     the channels are the rows of A, so a lane that holds 16-byte pieces of the keys 2t, 2t + 1,
 //     2t + 8, 2t + 9 only interleaves key pairs (one byte permute per register).
-//   - S has the heads on M (rows >= gs are zero) and the keys on N, so its accumulator is
-//     directly the B operand of O^T, whose N = 8 columns are the heads: nothing is exchanged
-//     between lanes but the maxima.
+//   - S^T = K Q^T has the keys on M = 16 and the heads on N = 8; its weights become the B operand
+//     of O^T = V^T P^T (channels on M, heads on N) by one 8 x 8 transposition per 8 keys.
 //   - Page ids are loaded two steps ahead of the rows they locate, the rows one step ahead of
 //     their use.
 // P is used as two parts (hi + lo): bf16 parts leave 2^-17 of it, f16 parts 2^-22, so that the
@@ -145,6 +144,12 @@ __device__ __forceinline__ uint32_t pack_f16(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// An 8 x 8 tile of 16-bit numbers transposed: from row lane / 4, columns 2 (lane % 4) + {0, 1}.
+__device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+  return r;
+}
 // Two weights as hi + lo parts of the matrix operand's type.
 template <bool K8>
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
@@ -213,12 +218,12 @@ constexpr int kPaRing = kPaStages * kPaStage;
 // Keys [k0, k1) of a row, over the CTA's warps: the state of every head is left in shared
 // memory (mo [warps][8][d], ml [warps][8][2], which reuse the rings). Ends with the state of
 // all warps written (a barrier).
-template <bool K8, bool kList>
+template <bool K8, bool kList, bool kPair>
 __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKeys& rk,
                                              const uint16_t* q, int gs, int k0, int k1,
                                              char* smem, float* mo, float* ml) {
   constexpr int S = K8 ? 32 : 16;       // keys of a warp's step
-  constexpr int NT = S / 8;             // 8-key tiles of S
+  constexpr int NM = S / 16;            // 16-key tiles of S^T
   constexpr int RB = K8 ? kD : 2 * kD;  // bytes of a cache row
   constexpr int RC = RB / 16;           // 16-byte chunks of a row
   constexpr int NS = kPaStages;
@@ -284,16 +289,18 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
     blk2 = bl[NS];
     j0 += (NS - 1) * stride;
   }
-  // Query fragments (rows >= gs zero). bf16: MMA i takes the channels 16i..16i+15 in order;
-  // 8-bit: k = 2tq, 2tq + 1, 2tq + 8, 2tq + 9 are the channels 16i + 4tq + {0, 1, 2, 3}.
+  // Query fragments of column gq: head gq, or with kPair head gq % 4 (columns without a head are
+  // zero). bf16: MMA i takes the channels 16i..16i+15 in order; 8-bit: k = 2tq, 2tq + 1, 2tq + 8,
+  // 2tq + 9 are the channels 16i + 4tq + {0, 1, 2, 3}.
   // A negative scale goes into the queries' signs, so that the largest product is the largest
   // logit: logit = hs * product in log2 units, hs > 0 (a scale of 0 becomes the smallest number).
   uint32_t qa[8][2];
   float hs = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
   {
-    const bool hv = gq < gs;
+    const int head = kPair ? gq & 3 : gq;
+    const bool hv = head < gs;
     const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-    const uint32_t* q2 = reinterpret_cast<const uint32_t*>(q + (size_t)(hv ? gq : 0) * kD);
+    const uint32_t* q2 = reinterpret_cast<const uint32_t*>(q + (size_t)(hv ? head : 0) * kD);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       qa[i][0] = hv ? q2[8 * i + (K8 ? 2 * tq : tq)] ^ sign : 0u;
@@ -318,8 +325,10 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
     }
   }
 
-  float m_run = -INFINITY, l_run = 0.f;  // head gq (m_run the same on its 4 lanes)
-  uint32_t e_run = 0u;                   // 8-bit: largest exponent byte of a value so far
+  // Of the columns 2tq + e (m_run the same on the column's 8 lanes).
+  const float hse[2] = {__shfl_sync(kFull, hs, 8 * tq), __shfl_sync(kFull, hs, 8 * tq + 4)};
+  float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+  uint32_t e_run = 0u;  // 8-bit: largest exponent byte of a value so far
   float oacc[8][4];
 #pragma unroll
   for (int i = 0; i < 8; ++i) oacc[i][0] = oacc[i][1] = oacc[i][2] = oacc[i][3] = 0.f;
@@ -346,85 +355,101 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
     }
     const unsigned ok = __ballot_sync(kFull, rq[0] != kNoRow);
 
-    float sacc[NT][4];
+    // S^T = K Q^T, 16 keys at a time: sacc[m][2r + e] is key 16m + 8r + gq, column 2tq + e.
+    float sacc[NM][4];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
+    for (int m = 0; m < NM; ++m) {
       float s2[4] = {0.f, 0.f, 0.f, 0.f};  // two chains of 4: less truncation, and overlap
-      sacc[j][0] = sacc[j][1] = sacc[j][2] = sacc[j][3] = 0.f;
-      const int r = 8 * j + l8;
+      sacc[m][0] = sacc[m][1] = sacc[m][2] = sacc[m][3] = 0.f;
+      const int r = 16 * m + (mj & 1) * 8 + l8;
 #pragma unroll
-      for (int c = 0; c < RC; c += 4) {  // 4 chunks of 8 keys at a time
+      for (int c = 0; c < RC; c += 2) {  // chunks c, c + 1 of the keys 0-7 and 8-15
         uint32_t w[4];
-        ldsm_x4(ks + (uint32_t)(r * RB + (((c + mj) ^ l8) << 4)), w[0], w[1], w[2], w[3]);
+        ldsm_x4(ks + (uint32_t)(r * RB + (((c + (mj >> 1)) ^ l8) << 4)), w[0], w[1], w[2], w[3]);
         if constexpr (K8) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-          {
-            uint32_t b0, b1;
-            e4m3x4_to_f16x2(w[i], b0, b1);
-            mma_16816_f16((i & 1) ? s2 : sacc[j], qa[c + i][0], 0u, qa[c + i][1], 0u, b0, b1);
+          for (int i = 0; i < 2; ++i) {
+            uint32_t a0, a1, a2, a3;
+            e4m3x4_to_f16x2(w[2 * i], a0, a2);
+            e4m3x4_to_f16x2(w[2 * i + 1], a1, a3);
+            mma_16816_f16(i ? s2 : sacc[m], a0, a1, a2, a3, qa[c + i][0], qa[c + i][1]);
           }
         } else {
-          mma_16816(sacc[j], qa[c / 2][0], 0u, qa[c / 2][1], 0u, w[0], w[1]);
-          mma_16816(s2, qa[c / 2 + 1][0], 0u, qa[c / 2 + 1][1], 0u, w[2], w[3]);
+          mma_16816((c & 2) ? s2 : sacc[m], w[0], w[1], w[2], w[3], qa[c / 2][0], qa[c / 2][1]);
         }
       }
-      sacc[j][0] += s2[0];
-      sacc[j][1] += s2[1];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sacc[m][i] += s2[i];
     }
 
-    // Products of head gq and the keys 8j + 2tq, 8j + 2tq + 1. 8-bit: the lane that located a
-    // key hands out 2^k_exp and what its value's weight is scaled by, as two bf16 numbers.
-    uint32_t e2[NT][2];
+    // 8-bit: the lane that located a key hands out 2^k_exp and what its value's weight is scaled
+    // by, as two bf16 numbers.
+    uint32_t ke[NM][2];
     uint32_t e_new = e_run;
     if constexpr (K8) {
       e_new = max(e_run, __reduce_max_sync(kFull, xv));
       const uint32_t mine = xk << 23 | (uint32_t)max(127 + 14 + (int)xv - (int)e_new, 0) << 7;
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int m = 0; m < NM; ++m)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          e2[j][i] = __shfl_sync(kFull, mine, 8 * j + 2 * tq + i);
-          sacc[j][i] *= __uint_as_float(e2[j][i] & 0xffff0000u);
+        for (int r = 0; r < 2; ++r) {
+          ke[m][r] = __shfl_sync(kFull, mine, 16 * m + 8 * r + gq);
+          const float s = __uint_as_float(ke[m][r] & 0xffff0000u);
+          sacc[m][2 * r] *= s;
+          sacc[m][2 * r + 1] *= s;
         }
     }
     if (ok != kFull) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+      for (int m = 0; m < NM; ++m)
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          if (!(ok >> (8 * j + 2 * tq + i) & 1u)) sacc[j][i] = -INFINITY;
+        for (int r = 0; r < 2; ++r)
+          if (!(ok >> (16 * m + 8 * r + gq) & 1u)) sacc[m][2 * r] = sacc[m][2 * r + 1] = -INFINITY;
     }
-    float mx = fmaxf(sacc[0][0], sacc[0][1]);
+    float corr[2], mu[2];
 #pragma unroll
-    for (int j = 1; j < NT; ++j) mx = fmaxf(mx, fmaxf(sacc[j][0], sacc[j][1]));
-    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
-    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
-    const float m_new = fmaxf(m_run, mx);
-    // What the sums so far are scaled by: head gq's, and those of the columns 2tq, 2tq + 1.
-    const float corr = m_new > m_run ? ex2((m_run - m_new) * hs) : 1.f;
-    l_run *= corr;
-    float ca = __shfl_sync(kFull, corr, 8 * tq), cb = __shfl_sync(kFull, corr, 8 * tq + 4);
+    for (int e = 0; e < 2; ++e) {
+      float mx = fmaxf(sacc[0][e], sacc[0][2 + e]);
+#pragma unroll
+      for (int m = 1; m < NM; ++m) mx = fmaxf(mx, fmaxf(sacc[m][e], sacc[m][2 + e]));
+#pragma unroll
+      for (int o = 4; o <= 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+      // What the column's sums so far are scaled by.
+      corr[e] = mx > m_run[e] ? ex2((m_run[e] - mx) * hse[e]) : 1.f;
+      m_run[e] = fmaxf(m_run[e], mx);
+      l_run[e] *= corr[e];
+      mu[e] = m_run[e] == -INFINITY ? 0.f : -m_run[e] * hse[e];
+    }
     if constexpr (K8) {
       const float ec = exp_scale((uint32_t)max(127 + (int)e_run - (int)e_new, 0));
-      ca *= ec;
-      cb *= ec;
+      corr[0] *= ec;
+      corr[1] *= ec;
       e_run = e_new;
     }
-    m_run = m_new;
-    const float mu = m_run == -INFINITY ? 0.f : -m_run * hs;
-    uint32_t ph[NT], pl[NT];
+    // Weights, as two parts of the operands' type, transposed into B operands: ph[i] holds the
+    // keys 8i + 2tq, 8i + 2tq + 1 of column gq. kPair: columns 0-3 take the first parts, 4-7 the
+    // second, in one product.
+    uint32_t ph[2 * NM], pl[2 * NM];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      float p[2];
+    for (int m = 0; m < NM; ++m)
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        p[i] = ex2(fmaf(sacc[j][i], hs, mu));
-        l_run += p[i];
-        if constexpr (K8) p[i] *= __uint_as_float(e2[j][i] << 16);
+      for (int r = 0; r < 2; ++r) {
+        float p[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          p[e] = ex2(fmaf(sacc[m][2 * r + e], hse[e], mu[e]));
+          l_run[e] += p[e];
+          if constexpr (K8) p[e] *= __uint_as_float(ke[m][r] << 16);
+        }
+        uint32_t hi, lo;
+        split_pair<K8>(p[0], p[1], hi, lo);
+        if constexpr (kPair) {
+          ph[2 * m + r] = movmatrix(tq < 2 ? hi : lo);
+        } else {
+          ph[2 * m + r] = movmatrix(hi);
+          pl[2 * m + r] = movmatrix(lo);
+        }
       }
-      split_pair<K8>(p[0], p[1], ph[j], pl[j]);
-    }
     // O^T = corr O^T + V^T P^T. The step's products are summed from zero and added in fp32: the
     // matrix units truncate when they add to an accumulator, and over thousands of steps that
     // is a bias (8e-6 of the output at 128K keys; 1e-6 this way).
@@ -442,19 +467,19 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
           e4m3x4_to_f16x2(__byte_perm(w[2 * h], 0u, 0x3120), a0, a1);
           e4m3x4_to_f16x2(__byte_perm(w[2 * h + 1], 0u, 0x3120), a2, a3);
           mma_16816_f16(o, a0, a1, a2, a3, ph[2 * h], ph[2 * h + 1]);
-          mma_16816_f16(o, a0, a1, a2, a3, pl[2 * h], pl[2 * h + 1]);
+          if constexpr (!kPair) mma_16816_f16(o, a0, a1, a2, a3, pl[2 * h], pl[2 * h + 1]);
         }
       } else {
         // Chunks 2i, 2i + 1 of keys 0-7, then of keys 8-15.
         const int r = (mj >> 1) * 8 + l8;
         ldsm_x4_t(vs + (uint32_t)(r * RB + (((2 * i + (mj & 1)) ^ l8) << 4)), w[0], w[1], w[2], w[3]);
         mma_16816(o, w[0], w[1], w[2], w[3], ph[0], ph[1]);
-        mma_16816(o, w[0], w[1], w[2], w[3], pl[0], pl[1]);
+        if constexpr (!kPair) mma_16816(o, w[0], w[1], w[2], w[3], pl[0], pl[1]);
       }
-      oacc[i][0] = fmaf(oacc[i][0], ca, o[0]);
-      oacc[i][1] = fmaf(oacc[i][1], cb, o[1]);
-      oacc[i][2] = fmaf(oacc[i][2], ca, o[2]);
-      oacc[i][3] = fmaf(oacc[i][3], cb, o[3]);
+      oacc[i][0] = fmaf(oacc[i][0], corr[0], o[0]);
+      oacc[i][1] = fmaf(oacc[i][1], corr[1], o[1]);
+      oacc[i][2] = fmaf(oacc[i][2], corr[0], o[2]);
+      oacc[i][3] = fmaf(oacc[i][3], corr[1], o[3]);
     }
 #pragma unroll
     for (int i = 0; i < NS - 1; ++i) rq[i] = rq[i + 1];
@@ -463,23 +488,34 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
   cp_async_wait<0>();
   __syncthreads();  // every warp is done with its ring: mo and ml lie over them
 
-  l_run += __shfl_xor_sync(kFull, l_run, 1);
-  l_run += __shfl_xor_sync(kFull, l_run, 2);
-  // oacc[i]: channel c0 (elements 0, 1) and c1 (2, 3) of the heads 2tq, 2tq + 1.
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int o = 4; o <= 16; o <<= 1) l_run[e] += __shfl_xor_sync(kFull, l_run[e], o);
+  // oacc[i]: channel c0 (elements 0, 1) and c1 (2, 3) of the columns 2tq, 2tq + 1.
   // 8-bit: 2^-14 and the running exponent, one after the other (2^(e_run - 141) may be subnormal).
   const float os = K8 ? 6.103515625e-05f : 1.f, oe = K8 ? exp_scale(e_run) : 1.f;
   float* mw = mo + (size_t)warp * kMaxGroup * kD;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
+    if constexpr (kPair) {  // column c + 4 is the second part of column c
+#pragma unroll
+      for (int j = 0; j < 4; ++j) oacc[i][j] += __shfl_xor_sync(kFull, oacc[i][j], 2);
+    }
     const int c0 = K8 ? 16 * i + 2 * gq : 16 * i + gq, c1 = K8 ? c0 + 1 : c0 + 8;
-    mw[(2 * tq) * kD + c0] = oacc[i][0] * os * oe;
-    mw[(2 * tq + 1) * kD + c0] = oacc[i][1] * os * oe;
-    mw[(2 * tq) * kD + c1] = oacc[i][2] * os * oe;
-    mw[(2 * tq + 1) * kD + c1] = oacc[i][3] * os * oe;
+    if (!kPair || tq < 2) {
+      mw[(2 * tq) * kD + c0] = oacc[i][0] * os * oe;
+      mw[(2 * tq + 1) * kD + c0] = oacc[i][1] * os * oe;
+      mw[(2 * tq) * kD + c1] = oacc[i][2] * os * oe;
+      mw[(2 * tq + 1) * kD + c1] = oacc[i][3] * os * oe;
+    }
   }
-  if (tq == 0) {
-    ml[(warp * kMaxGroup + gq) * 2] = m_run * hs;  // in log2 units
-    ml[(warp * kMaxGroup + gq) * 2 + 1] = l_run;
+  if (gq == 0) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      ml[(warp * kMaxGroup + 2 * tq + e) * 2] = m_run[e] * hse[e];  // in log2 units
+      ml[(warp * kMaxGroup + 2 * tq + e) * 2 + 1] = l_run[e];
+    }
   }
   __syncthreads();
 }
@@ -556,7 +592,7 @@ __device__ __forceinline__ void join_warps(const float* mo, const float* ml, int
 }
 
 // Even shares of all rows' keys (see the head of this file).
-template <bool K8, bool kList>
+template <bool K8, bool kList, bool kPair>
 __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(PageAttnArgs a) {
   extern __shared__ float4 pa_smem[];
   __shared__ int sh[40];
@@ -597,7 +633,7 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
     if (!kList && a.k_new != nullptr && off + take == ub && rk.n > 0) append_row<K8>(a, rk, b);
     __syncthreads();  // the new row is visible; the previous segment's state has been read
     const size_t head0 = (size_t)bt * a.Hq + (size_t)r * gs;
-    page_segment<K8, kList>(a, rk, a.q + head0 * kD, gs, off * kUnitKeys,
+    page_segment<K8, kList, kPair>(a, rk, a.q + head0 * kD, gs, off * kUnitKeys,
                             min(rk.n, (off + take) * kUnitKeys),
                             reinterpret_cast<char*>(pa_smem), mo, ml);
     const bool whole = off == 0 && take == ub;
@@ -630,7 +666,7 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
 // One cluster per row: its CTAs take equal parts of the row's keys and are joined through
 // distributed shared memory, each rank writing its share of the row's outputs. One launch, and no
 // partials in global memory.
-template <bool K8, bool kList>
+template <bool K8, bool kList, bool kPair>
 __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_cluster_kernel(PageAttnArgs a) {
   namespace cg = cooperative_groups;
   extern __shared__ float4 pa_smem[];
@@ -648,7 +684,7 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_cluster_kernel(
   if (!kList && a.k_new != nullptr && k0 < k1 && k1 == rk.n) append_row<K8>(a, rk, b);
   __syncthreads();
   const size_t head0 = (size_t)bt * a.Hq + (size_t)r * gs;
-  page_segment<K8, kList>(a, rk, a.q + head0 * kD, gs, k0, k1, reinterpret_cast<char*>(pa_smem), mo,
+  page_segment<K8, kList, kPair>(a, rk, a.q + head0 * kD, gs, k0, k1, reinterpret_cast<char*>(pa_smem), mo,
                           ml);
   for (int i = tid; i < gs * kD; i += kPaThreads) {
     const int h = i / kD, ch = i % kD;
