@@ -1,4 +1,5 @@
-"""Build the retrieval library in-tree: nvcc -> hash_hierarchical_top_b200/libhhr.so (sm_100a).
+"""Build the retrieval library in-tree: nvcc -> hash_hierarchical_top_b200/libhhr.so (sm_100a),
+and the Python marshalling module beside it: g++ -> hash_hierarchical_top_b200/_binding.so.
 
 Run ``python -m hash_hierarchical_top_b200.build`` (or call ``build()``). The
 library is a single CUDA translation unit; nvcc cross-compiles it without a GPU.
@@ -8,11 +9,13 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libhhr.so")
+BINDING = os.path.join(HERE, "_binding.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -27,12 +30,45 @@ def sources():
             if f.endswith((".cu", ".cuh"))] + [os.path.join(ROOT, "include", "hhr.h")]
 
 
+def _fresh(target, srcs):
+    return os.path.exists(target) and all(os.path.getmtime(s) <= os.path.getmtime(target)
+                                          for s in srcs)
+
+
+def build_binding(force: bool = False):
+    """Start compiling _binding.so (against the installed torch's headers) if it is missing or
+    older than its sources; returns the process, or None."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and _fresh(BINDING, [src, os.path.join(ROOT, "include", "hhr.h")]):
+        return None
+    import torch
+    from torch.utils.cpp_extension import CUDA_HOME, include_paths
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = include_paths() + [sysconfig.get_paths()["include"],
+                             os.path.join(CUDA_HOME or "/usr/local/cuda", "include")]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{i}" for i in inc), "-o", BINDING + ".tmp", src, f"-L{libs}",
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    return subprocess.Popen(cmd)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libhhr.so if it is missing or older than any source; return its path."""
-    if not force and os.path.exists(LIB):
-        t_lib = os.path.getmtime(LIB)
-        if all(os.path.getmtime(s) <= t_lib for s in sources()):
-            return LIB
+    """Compile libhhr.so and _binding.so where they are missing or older than a source; return
+    the library's path."""
+    binding = build_binding(force)
+    try:
+        return _build_lib(force, verbose)
+    finally:
+        if binding is not None:
+            if binding.wait() != 0:
+                raise RuntimeError("building _binding.so failed")
+            os.replace(BINDING + ".tmp", BINDING)
+
+
+def _build_lib(force: bool, verbose: bool) -> str:
+    if not force and _fresh(LIB, sources()):
+        return LIB
     nvcc = os.environ.get("NVCC", "nvcc")
     if os.path.exists("/usr/local/cuda/bin/nvcc") and nvcc == "nvcc":
         nvcc = "/usr/local/cuda/bin/nvcc"

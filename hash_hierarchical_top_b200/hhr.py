@@ -9,6 +9,8 @@ there is no fallback of any kind when it is missing.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -303,108 +305,50 @@ def hhr_decode_step(d, q, k_new, v_new, k_cache, v_cache, page_table, seq_len, R
 
 
 # ------------------------------------------------------------------------------------------
-# The 8-bit cache, dense paged attention and block-sparse attention. These calls also check
-# their tensors' sizes and that all of them are on the current device.
+# The 8-bit cache, dense paged attention and block-sparse attention. Their marshalling is
+# compiled (csrc/binding.cpp): it also checks the tensors' sizes, and that all of them are on the
+# current device.
 
-E4M3 = (torch.float8_e4m3fn, torch.uint8)
-U8 = (torch.uint8,)
-OUT = (torch.float32, torch.bfloat16)
-
-
-def _t(t, dtypes, name, n, dev):
-    """Device address of a contiguous tensor of at least ``n`` elements on device ``dev``."""
-    if t is None:
-        return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}, the current device")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {dtypes}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    if t.numel() < n:
-        raise ValueError(f"{name}: {t.numel()} elements, expected at least {n}")
-    return t.data_ptr()
+_binding = None
 
 
-def _here(stream):
-    """(current device, raw stream handle) of a call."""
-    dev = torch._C._cuda_getDevice()
-    if stream is None:
-        return dev, torch._C._cuda_getCurrentRawStream(dev)
-    return dev, stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-
-
-def _cache_pair(d, k, v, k_exp, v_exp, dev):
-    """Addresses of a bf16 cache (no exponents) or an 8-bit one, after checking their sizes."""
-    rows = d.n_phys_pages * d.n_kv_heads * d.page_size
-    kinds = _BF16 if k_exp is None and v_exp is None else E4M3
-    return (_t(k, kinds, "k", rows * d.head_dim, dev), _t(v, kinds, "v", rows * d.head_dim, dev),
-            _t(k_exp, U8, "k_exp", rows, dev), _t(v_exp, U8, "v_exp", rows, dev))
-
-
-def _new_rows(d, t, name, dev):
-    """(address, max_new, token stride) of new rows [B][max_new][G][d] or [B][G][d]: channels
-    and heads contiguous, tokens evenly spaced over all sequences."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: expected a torch tensor")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}, the current device")
-    if t.dtype not in _BF16:
-        raise TypeError(f"{name}: dtype {t.dtype} not in {_BF16}")
-    if t.dim() == 3:
-        t = t.unsqueeze(1)
-    B, G, D = d.batch, d.n_kv_heads, d.head_dim
-    if t.dim() != 4 or t.shape[0] != B or t.shape[2] != G or t.shape[3] != D:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected ({B}, n, {G}, {D})")
-    n, (sb, st, sg, sd) = t.shape[1], t.stride()
-    if n == 1:  # one token a sequence: the tokens' spacing is the sequences'
-        st = sb if B > 1 else G * D
-    if sd != 1 or (G > 1 and sg != D) or (B > 1 and n > 0 and sb != n * st):
-        raise ValueError(f"{name}: strides {t.stride()} are not those of evenly spaced tokens")
-    return t.data_ptr(), n, st
+def _native():
+    """The loaded _binding.so, bound to the loaded library (raises if it has not been built)."""
+    global _binding
+    if _binding is None:
+        path = os.path.join(HERE, "_binding.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with "
+                               "`python -m hash_hierarchical_top_b200.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_binding", path)
+        spec = importlib.util.spec_from_loader("_binding", loader)
+        module = importlib.util.module_from_spec(spec)
+        loader.exec_module(module)
+        _binding = module
+    L = lib()
+    if getattr(L, "_bound", None) is not _binding:
+        _binding.bind(*(ctypes.cast(getattr(L, "hhr_" + n), ctypes.c_void_p).value for n in (
+            "append_kv8", "read_kv8", "paged_attn", "block_select", "block_attn")))
+        L._bound = _binding
+    return _binding
 
 
 def hhr_append_kv8(d, k_new, v_new, start, n_new, page_table, k, v, k_exp, v_exp,
                    block_mean=None, stream=None):
     """Quantise new rows [B][max_new][G][d] (or [B][G][d]; slices of a wider product are taken
     as they are) into an 8-bit cache; ``block_mean`` is kept up to date when given."""
-    dev, s = _here(stream)
-    pk, max_new, st = _new_rows(d, k_new, "k_new", dev)
-    pv, max_v, st_v = _new_rows(d, v_new, "v_new", dev)
-    if (max_v, st_v) != (max_new, st):
-        raise ValueError("k_new and v_new: expected the same shape and strides")
-    if k_exp is None or v_exp is None:
-        raise ValueError("k_exp, v_exp: an 8-bit cache has exponents")
-    if max_new == 0:  # no element, hence no address to pass
-        return
-    c = _cache_pair(d, k, v, k_exp, v_exp, dev)
-    _check("hhr_append_kv8", lib().hhr_append_kv8(
-        ctypes.byref(d), pk, pv, st, _t(start, I32, "start", d.batch, dev),
-        _t(n_new, I32, "n_new", d.batch, dev), max_new,
-        _t(page_table, I32, "page_table", d.batch * d.max_pages_per_seq, dev), *c,
-        _t(block_mean, F32, "block_mean", d.n_phys_pages * d.n_kv_heads * d.head_dim, dev), s))
+    st = _native().append_kv8(d, k_new, v_new, start, n_new, page_table, k, v, k_exp, v_exp,
+                              block_mean, stream)
+    if st:
+        raise HHRError("hhr_append_kv8", st)
 
 
 def hhr_read_kv8(d, k, v, k_exp, v_exp, page_table, start, n, k_out, v_out, stream=None):
     """Read positions [start, start + n) of each sequence of an 8-bit cache into bf16
     [B][max_n][G][d]; rows past n are left as they were."""
-    dev, s = _here(stream)
-    if k_out.dim() != 4 or k_out.shape != v_out.shape:
-        raise ValueError("k_out, v_out: expected [B][max_n][G][d], both alike")
-    if k_exp is None or v_exp is None:
-        raise ValueError("k_exp, v_exp: an 8-bit cache has exponents")
-    max_n = k_out.shape[1]
-    if max_n == 0:
-        return
-    c = _cache_pair(d, k, v, k_exp, v_exp, dev)
-    rows = d.batch * max_n * d.n_kv_heads * d.head_dim
-    _check("hhr_read_kv8", lib().hhr_read_kv8(
-        ctypes.byref(d), *c,
-        _t(page_table, I32, "page_table", d.batch * d.max_pages_per_seq, dev),
-        _t(start, I32, "start", d.batch, dev), _t(n, I32, "n", d.batch, dev), max_n,
-        _t(k_out, _BF16, "k_out", rows, dev), _t(v_out, _BF16, "v_out", rows, dev), s))
+    st = _native().read_kv8(d, k, v, k_exp, v_exp, page_table, start, n, k_out, v_out, stream)
+    if st:
+        raise HHRError("hhr_read_kv8", st)
 
 
 def hhr_paged_attn_workspace_bytes(d) -> int:
@@ -414,27 +358,10 @@ def hhr_paged_attn_workspace_bytes(d) -> int:
 def hhr_paged_attn(d, q, k_new, v_new, k_cache, v_cache, k_exp, v_exp, page_table, seq_len, scale,
                    out, workspace, lse=None, stream=None):
     """Dense attention of one new token per sequence; ``out`` [B][Hq][d] is f32 or bf16."""
-    dev, s = _here(stream)
-    B, heads = d.batch, d.batch * d.n_q_heads
-    new = B * d.n_kv_heads * d.head_dim
-    c = _cache_pair(d, k_cache, v_cache, k_exp, v_exp, dev)
-    _check("hhr_paged_attn", lib().hhr_paged_attn(
-        ctypes.byref(d), _t(q, _BF16, "q", heads * d.head_dim, dev),
-        _t(k_new, _BF16, "k_new", new, dev), _t(v_new, _BF16, "v_new", new, dev), *c,
-        _t(page_table, I32, "page_table", B * d.max_pages_per_seq, dev),
-        _t(seq_len, I32, "seq_len", B, dev), scale,
-        _t(out, OUT, "out", heads * d.head_dim, dev), int(out.dtype == torch.bfloat16),
-        _t(lse, F32, "lse", heads, dev), _t(workspace, U8, "workspace", 0, dev),
-        workspace.numel(), s))
-
-
-def _queries(d, q):
-    """Queries per sequence of q [B][T][Hq][d]."""
-    if not isinstance(q, torch.Tensor):
-        raise TypeError("q: expected a torch tensor")
-    if q.dim() != 4 or q.shape[0] != d.batch or q.shape[2] != d.n_q_heads:
-        raise ValueError(f"q: shape {tuple(q.shape)}, expected [B][T][Hq][d]")
-    return q.shape[1]
+    st = _native().paged_attn(d, q, k_new, v_new, k_cache, v_cache, k_exp, v_exp, page_table,
+                              seq_len, scale, out, workspace, lse, stream)
+    if st:
+        raise HHRError("hhr_paged_attn", st)
 
 
 def hhr_block_select_workspace_bytes(d, n_queries) -> int:
@@ -444,19 +371,10 @@ def hhr_block_select_workspace_bytes(d, n_queries) -> int:
 def hhr_block_select(d, q, seq_len, q_pos, page_table, block_mean, m_pages, out_blocks, out_count,
                      workspace, stream=None, opts=None):
     """The ``m_pages`` best blocks of each query of q [B][T][Hq][d] and KV group."""
-    dev, s = _here(stream)
-    T, B = _queries(d, q), d.batch
-    rows = B * T * sel_rows(d)
-    _check("hhr_block_select", lib().hhr_block_select(
-        ctypes.byref(d), T, _t(q, _BF16, "q", B * T * d.n_q_heads * d.head_dim, dev),
-        _t(seq_len, I32, "seq_len", B, dev), _t(q_pos, I32, "q_pos", B * T, dev),
-        _t(page_table, I32, "page_table", B * d.max_pages_per_seq, dev),
-        _t(block_mean, F32, "block_mean", d.n_phys_pages * d.n_kv_heads * d.head_dim, dev),
-        int(m_pages), ctypes.byref(opts) if opts is not None else None,
-        _t(out_blocks, I32, "out_blocks",
-           rows * max(0, min(int(m_pages), d.max_pages_per_seq)), dev),
-        _t(out_count, I32, "out_count", rows, dev), _t(workspace, U8, "workspace", 0, dev),
-        workspace.numel(), s))
+    st = _native().block_select(d, q, seq_len, q_pos, page_table, block_mean, m_pages, opts,
+                                out_blocks, out_count, workspace, stream)
+    if st:
+        raise HHRError("hhr_block_select", st)
 
 
 def hhr_block_attn_workspace_bytes(d, n_queries, m_max) -> int:
@@ -467,16 +385,7 @@ def hhr_block_attn(d, q, k_cache, v_cache, k_exp, v_exp, page_table, seq_len, q_
                    block_count, scale, out, workspace, lse=None, stream=None):
     """Attention of each query of q [B][T][Hq][d] over its own blocks [B][T][rows][m_max];
     ``out`` [B][T][Hq][d] is f32 or bf16."""
-    dev, s = _here(stream)
-    T, B = _queries(d, q), d.batch
-    rows, heads, m_max = B * T * sel_rows(d), B * T * d.n_q_heads, blocks.shape[-1]
-    c = _cache_pair(d, k_cache, v_cache, k_exp, v_exp, dev)
-    _check("hhr_block_attn", lib().hhr_block_attn(
-        ctypes.byref(d), T, _t(q, _BF16, "q", heads * d.head_dim, dev), *c,
-        _t(page_table, I32, "page_table", B * d.max_pages_per_seq, dev),
-        _t(seq_len, I32, "seq_len", B, dev), _t(q_pos, I32, "q_pos", B * T, dev),
-        _t(blocks, I32, "blocks", rows * m_max, dev),
-        _t(block_count, I32, "block_count", rows, dev), m_max, scale,
-        _t(out, OUT, "out", heads * d.head_dim, dev), int(out.dtype == torch.bfloat16),
-        _t(lse, F32, "lse", heads, dev), _t(workspace, U8, "workspace", 0, dev),
-        workspace.numel(), s))
+    st = _native().block_attn(d, q, k_cache, v_cache, k_exp, v_exp, page_table, seq_len, q_pos,
+                              blocks, block_count, scale, out, workspace, lse, stream)
+    if st:
+        raise HHRError("hhr_block_attn", st)

@@ -163,34 +163,43 @@ def test_block_arguments(L):
     assert block(L, _d(page_size=256, n_phys_pages=1 << 21)) == UNS
 
 
-def test_binding_checks_its_tensors():
-    cpu = torch.zeros(2, 4, 8, 128, dtype=torch.bfloat16)
-    with pytest.raises(ValueError, match="current device"):
-        hhr._t(cpu, hhr._BF16, "q", 1, 0)
-    with pytest.raises(TypeError):
-        hhr._t([1], hhr.I32, "x", 1, 0)
-    assert hhr._t(None, hhr.I32, "x", 1, 0) is None
-    # Host tensors are on "device" -1: the remaining checks, without a GPU.
-    with pytest.raises(TypeError):
-        hhr._t(cpu, hhr.I32, "x", 1, -1)
-    with pytest.raises(ValueError, match="contiguous"):
-        hhr._t(cpu.transpose(0, 1), hhr._BF16, "x", 1, -1)
-    with pytest.raises(ValueError, match="elements"):
-        hhr._t(cpu, hhr._BF16, "x", cpu.numel() + 1, -1)
+# The binding: every call refuses host tensors and things that are no tensors, before anything
+# else of theirs is used. (What it checks of CUDA tensors is tested in test_gpu_binding.py.)
+HOST = torch.zeros(2, 4, 8, 128, dtype=torch.bfloat16)
+BINDING_CALLS = {
+    "hhr_append_kv8": lambda d, t: hhr.hhr_append_kv8(d, t, t, t, t, t, t, t, t, t),
+    "hhr_read_kv8": lambda d, t: hhr.hhr_read_kv8(d, t, t, t, t, t, t, t, t, t),
+    "hhr_paged_attn": lambda d, t: hhr.hhr_paged_attn(d, t, None, None, t, t, None, None, t, t,
+                                                      0.1, t, t),
+    "hhr_block_select": lambda d, t: hhr.hhr_block_select(d, t, t, t, t, t, 4, t, t, t),
+    "hhr_block_attn": lambda d, t: hhr.hhr_block_attn(d, t, t, t, None, None, t, t, t, t, t, 0.1,
+                                                      t, t),
+}
 
 
-def test_binding_takes_slices_of_a_fused_product():
-    d = _d()
-    qkv = torch.zeros(2, 5, 48, 128, dtype=torch.bfloat16)
-    k = qkv[:, :, 32:40]
-    assert hhr._new_rows(d, k, "k", -1) == (k.data_ptr(), 5, 48 * 128)
-    assert hhr._new_rows(d, k[:, 0], "k", -1)[1:] == (1, 5 * 48 * 128)
-    assert hhr._new_rows(d, k[:, 4:], "k", -1)[1:] == (1, 5 * 48 * 128)
-    assert hhr._new_rows(d, k.contiguous(), "k", -1)[1:] == (5, 8 * 128)
-    for bad in (k[:, 1:4],                              # sequences apart by more than their tokens
-                qkv[:, :, 32:48:2], qkv[:, :, 32:39], qkv[:1, :, 32:40],
-                k.transpose(2, 3), qkv[:, 0, 0]):
-        with pytest.raises(ValueError):
-            hhr._new_rows(d, bad, "k", -1)
+@pytest.mark.parametrize("name", sorted(BINDING_CALLS))
+def test_binding_refuses_what_is_no_cuda_tensor(L, name):
+    call = BINDING_CALLS[name]
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        call(_d(), HOST)
+    with pytest.raises(TypeError, match="torch tensor"):
+        call(_d(), [1, 2])
+    with pytest.raises(TypeError, match="dims"):
+        call(b"not dims", HOST)
     with pytest.raises(TypeError):
-        hhr._new_rows(d, k.float(), "k", -1)
+        call(None, HOST)
+
+
+def test_binding_module_is_required(L, monkeypatch, tmp_path):
+    monkeypatch.setattr(hhr, "HERE", str(tmp_path))
+    monkeypatch.setattr(hhr, "_binding", None)
+    with pytest.raises(RuntimeError, match="missing"):
+        hhr._native()
+
+
+def test_binding_follows_a_reloaded_library(L, monkeypatch):
+    """The module calls the library that hhr.lib() has loaded, also after it is loaded anew."""
+    module = hhr._native()
+    assert hhr.lib()._bound is module
+    monkeypatch.setattr(hhr, "_lib", None)
+    assert hhr._native() is module and hhr.lib()._bound is module
