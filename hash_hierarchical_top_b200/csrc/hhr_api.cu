@@ -963,6 +963,9 @@ namespace {
 bool g_smem_page[2][2][2][kMaxDevices],
     g_smem_cluster[2][2][2][kMaxDevices], g_smem_topm[2][kMaxDevices];
 
+// ceil(2^32 / n), the multiplier of a division by n (see page_of).
+uint32_t page_mul(int n) { return (uint32_t)((0x100000000ull + (unsigned)n - 1) / (unsigned)n); }
+
 // Cache rows are addressed with 32-bit row indices.
 bool rows_fit(const hhr_dims* d) {
   return (unsigned long long)d->n_phys_pages * d->n_kv_heads * d->page_size < 0xffffffffull;
@@ -1030,7 +1033,7 @@ int launch_page_attn(const hhr_dims* d, PageAttnArgs& a, bool k8, long long unit
   a.kv_div = kv_div(d); a.P = d->page_size; a.maxp = d->max_pages_per_seq;
   a.n_phys = d->n_phys_pages;
   a.n_rows = (uint32_t)a.n_phys * (uint32_t)a.G * (uint32_t)a.P;
-  a.p_mul = (uint32_t)((0x100000000ull + (unsigned)a.P - 1) / (unsigned)a.P);
+  a.p_mul = page_mul(a.P);
   a.n_ctas = page_ctas(units);
   const size_t gs = a.Hq / a.Gs;
   a.part_o = static_cast<float*>(workspace);
@@ -1166,10 +1169,10 @@ int hhr_read_kv8(const hhr_dims* d, const uint8_t* k, const uint8_t* v, const ui
   if (misaligned16({k_out, v_out})) return HHR_ERR_INVALID_ARG;
   if (max_n == 0) return HHR_OK;
   ReadArgs a{k, v, k_exp, v_exp, page_table, start, n, k_out, v_out, d->n_kv_heads, d->page_size,
-             d->max_pages_per_seq, d->n_phys_pages, max_n};
+             d->max_pages_per_seq, d->n_phys_pages, max_n, page_mul(d->page_size)};
   cudaStream_t s = (cudaStream_t)stream;
   prof_begin(HHR_KERNEL_READ, s);
-  read_kv8_kernel<<<dim3((unsigned)((max_n + (long long)kReadRows - 1) / kReadRows),
+  read_kv8_kernel<<<dim3((unsigned)((max_n + (long long)kReadTile - 1) / kReadTile),
                          d->n_kv_heads, d->batch),
                     kReadThreads, 0, s>>>(a);
   prof_end(HHR_KERNEL_READ, s);
@@ -1244,7 +1247,7 @@ int hhr_block_select(const hhr_dims* d, int n_queries, const uint16_t* q, const 
   const bool single = rows == 1 && d->n_kv_heads <= kBvMaxGroups;
   const long long stream_ctas = min(((long long)B * maxp * d->n_kv_heads + kBvItem - 1) / kBvItem,
                                     (long long)kBvCtasPerSm * sm_count());
-  a.g_mul = (uint32_t)((0x100000000ull + (unsigned)a.G - 1) / (unsigned)a.G);
+  a.g_mul = page_mul(a.G);
   // The choice: few threads per row of up to 1024 blocks (bound by barriers; more rows fit an
   // SM), more threads for longer rows.
   const int wide = maxp > HHR_BS_NARROW;

@@ -30,18 +30,20 @@ __device__ __forceinline__ uint32_t row_exponent(uint32_t top) {
   return (uint32_t)min(max(x, kExpMin), kExpMax);
 }
 
+// The larger of two pairs of bf16 numbers; a NaN only where both are.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // Largest |channel| (bf16 bits; NaNs ignored) of the row that 16 lanes hold, 8 channels each.
 __device__ __forceinline__ uint32_t row_top16(uint4 w, unsigned mask) {
-  auto mag = [](uint32_t two) {  // |.| of both halves; a NaN counts as 0
-    uint32_t lo = two & 0x7fffu, hi = (two >> 16) & 0x7fffu;
-    if (lo > 0x7f80u) lo = 0u;
-    if (hi > 0x7f80u) hi = 0u;
-    return max(lo, hi);
-  };
-  uint32_t m = max(max(mag(w.x), mag(w.y)), max(mag(w.z), mag(w.w)));
+  constexpr uint32_t kAbs = 0x7fff7fffu;
+  uint32_t m = max_bf16x2(max_bf16x2(w.x & kAbs, w.y & kAbs), max_bf16x2(w.z & kAbs, w.w & kAbs));
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(mask, m, o));
-  return m;
+  for (int o = 8; o > 0; o >>= 1) m = max_bf16x2(m, __shfl_xor_sync(mask, m, o));
+  const uint32_t lo = m & 0xffffu, hi = m >> 16;  // above 0x7f80: nothing but NaNs
+  return max(lo > 0x7f80u ? 0u : lo, hi > 0x7f80u ? 0u : hi);
 }
 
 // Two floats to e4m3 (to nearest even, saturating; NaN stays NaN): a in the low byte.
@@ -78,6 +80,15 @@ __device__ __forceinline__ uint2 quantise8(uint4 w, uint32_t x) {
   return r;
 }
 
+// 16 bytes that are read once; the load is issued where it stands.
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
 struct AppendArgs {
   const uint16_t* k_new;  // token i of sequence b, head g: + (b * max_new + i) * stride + g * d
   const uint16_t* v_new;
@@ -93,8 +104,15 @@ struct AppendArgs {
   int G, P, maxp, n_phys, max_new;
 };
 
-constexpr int kAppendThreads = 256;
-constexpr int kAppendRows = kAppendThreads / 16;  // rows in flight: 16 lanes each
+#ifndef HHR_APPEND_THREADS
+#define HHR_APPEND_THREADS 128
+#endif
+constexpr int kAppendThreads = HHR_APPEND_THREADS;
+constexpr int kAppendRows = kAppendThreads / 16;  // rows per pass: 16 lanes each
+#ifndef HHR_APPEND_UNROLL
+#define HHR_APPEND_UNROLL 2
+#endif
+constexpr int kAppendUnroll = HHR_APPEND_UNROLL;
 
 // One CTA per (touched page, KV group, sequence). 16 lanes quantise a row, 8 channels a lane.
 // With block_mean, the K rows that the page held before are read too, and the mean is taken
@@ -118,48 +136,70 @@ __global__ void __launch_bounds__(kAppendThreads) append_kv8_kernel(AppendArgs a
     if (tid == 0) flag_status(kStatusBadPage);
     return;
   }
+  // Not looked at before the first rows are on their way: one latency less per CTA.
   const int phys = a.page_table[(size_t)b * a.maxp + lp];
-  if (phys < 0 || phys >= a.n_phys) {
-    if (tid == 0) flag_status(kStatusBadPage);
-    return;
-  }
   const int pstart = (int)lp * P;
   const int t0 = max(s, pstart) - pstart, t1 = (int)min(e, (long long)pstart + P) - pstart;
   const int lane = tid & 15, sub = tid >> 4;
   const unsigned mask = 0xffffu << (tid & 16);  // the row's 16 lanes
-  const size_t row0 = ((size_t)phys * a.G + g) * P;
+  size_t row0 = 0;
   const size_t src0 = ((size_t)b * a.max_new + (pstart + t0 - s)) * a.stride + (size_t)g * kD + 8 * lane;
-  // V rows, then K rows.
-  for (int r = t0 + sub; r < t1; r += kAppendRows) {
-    const uint4 w = *reinterpret_cast<const uint4*>(a.v_new + src0 + (size_t)(r - t0) * a.stride);
-    const uint32_t x = row_exponent(row_top16(w, mask));
-    *reinterpret_cast<uint2*>(a.v + (row0 + r) * kD + 8 * lane) = quantise8(w, x);
-    if (lane == 0) a.v_exp[row0 + r] = (uint8_t)x;
-  }
   float sum[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) sum[i] = 0.f;
-  for (int r = (kMean ? 0 : t0) + sub; r < t1; r += kAppendRows) {
-    uint2 q;
-    uint32_t x;
-    if (kMean && r < t0) {
-      q = *reinterpret_cast<const uint2*>(a.k + (row0 + r) * kD + 8 * lane);
-      x = a.k_exp[row0 + r];
-    } else {
-      const uint4 w = *reinterpret_cast<const uint4*>(a.k_new + src0 + (size_t)(r - t0) * a.stride);
-      x = row_exponent(row_top16(w, mask));
-      q = quantise8(w, x);
-      *reinterpret_cast<uint2*>(a.k + (row0 + r) * kD + 8 * lane) = q;
-      if (lane == 0) a.k_exp[row0 + r] = (uint8_t)x;
-    }
-    if constexpr (kMean) {
-      const float sc = exp_scale(x);
+  auto add = [&](uint2 q, uint32_t x) {
+    const float sc = exp_scale(x);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = f16x2_to_f2(e4m3x2_to_f16x2((i < 2 ? q.x : q.y) >> (16 * (i & 1))));
-        sum[2 * i] = fmaf(f.x, sc, sum[2 * i]);
-        sum[2 * i + 1] = fmaf(f.y, sc, sum[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = f16x2_to_f2(e4m3x2_to_f16x2((i < 2 ? q.x : q.y) >> (16 * (i & 1))));
+      sum[2 * i] = fmaf(f.x, sc, sum[2 * i]);
+      sum[2 * i + 1] = fmaf(f.y, sc, sum[2 * i + 1]);
+    }
+  };
+  // New rows, kAppendUnroll of K and of V at a time: their loads are in flight together.
+  constexpr int U = kAppendUnroll;
+  for (int r0 = t0 + sub; r0 - sub < t1; r0 += U * kAppendRows) {  // the same steps for all threads
+    uint4 w[2][U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int r = r0 + u * kAppendRows;
+      const size_t src = src0 + (size_t)(r - t0) * a.stride;
+      w[0][u] = r < t1 ? ldg_stream(a.k_new + src) : make_uint4(0u, 0u, 0u, 0u);
+      w[1][u] = r < t1 ? ldg_stream(a.v_new + src) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (phys < 0 || phys >= a.n_phys) {
+      if (tid == 0) flag_status(kStatusBadPage);
+      return;
+    }
+    row0 = ((size_t)phys * a.G + g) * P;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const size_t row = row0 + r0 + u * kAppendRows;
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const uint32_t x = row_exponent(row_top16(w[kv][u], mask));
+        const uint2 q = quantise8(w[kv][u], x);
+        if (r0 + u * kAppendRows < t1) {
+          *reinterpret_cast<uint2*>((kv ? a.v : a.k) + row * kD + 8 * lane) = q;
+          if (lane == 0) (kv ? a.v_exp : a.k_exp)[row] = (uint8_t)x;
+          if (kMean && kv == 0) add(q, x);
+        }
       }
+    }
+  }
+  if constexpr (kMean) {
+    for (int r0 = sub; r0 < t0; r0 += U * kAppendRows) {  // what the page held before
+      uint2 q[U];
+      uint32_t x[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int r = r0 + u * kAppendRows;
+        q[u] = r < t0 ? *reinterpret_cast<const uint2*>(a.k + (row0 + r) * kD + 8 * lane)
+                      : make_uint2(0u, 0u);
+        x[u] = r < t0 ? a.k_exp[row0 + r] : 0u;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) add(q[u], x[u]);
     }
   }
   if constexpr (kMean) {
@@ -186,24 +226,33 @@ struct ReadArgs {
   uint16_t* k_out;  // [B][max_n][G][d]
   uint16_t* v_out;
   int G, P, maxp, n_phys, max_n;
+  uint32_t p_mul;  // ceil(2^32 / P)
 };
 
 constexpr int kReadThreads = 256;
-constexpr int kReadRows = kReadThreads / 8;  // rows per pass: 8 lanes each, 16 channels a lane
+constexpr int kReadRows = kReadThreads / 16;  // rows per pass: 16 lanes each, 8 channels a lane
+#ifndef HHR_READ_UNROLL
+#define HHR_READ_UNROLL 2
+#endif
+constexpr int kReadUnroll = HHR_READ_UNROLL, kReadTile = kReadRows * kReadUnroll;
 
-// 16 e4m3 channels times 2^(x - 127), as bf16 (exact).
-__device__ __forceinline__ void dequantise16(uint4 q, uint32_t x, uint4& lo, uint4& hi) {
+// 8 e4m3 channels times 2^(x - 127), as bf16 (exact).
+__device__ __forceinline__ uint4 dequantise8(uint2 q, uint32_t x) {
   const float s = exp_scale(x);
-  auto two = [&](uint32_t w, int half) {
-    const float2 f = f16x2_to_f2(e4m3x2_to_f16x2(w >> (16 * half)));
+  auto two = [&](uint32_t f16) {
+    const float2 f = f16x2_to_f2(f16);
     const __nv_bfloat162 r = __floats2bfloat162_rn(f.x * s, f.y * s);
     return *reinterpret_cast<const uint32_t*>(&r);
   };
-  lo = make_uint4(two(q.x, 0), two(q.x, 1), two(q.y, 0), two(q.y, 1));
-  hi = make_uint4(two(q.z, 0), two(q.z, 1), two(q.w, 0), two(q.w, 1));
+  uint32_t a, b, c, d;
+  e4m3x4_to_f16x2(q.x, a, b);
+  e4m3x4_to_f16x2(q.y, c, d);
+  return make_uint4(two(a), two(b), two(c), two(d));
 }
 
-// Grid (rows / kReadRows, KV group, sequence).
+// Grid (rows / kReadTile, KV group, sequence). A lane writes 16 bytes next to its neighbour's 16
+// (with 32 a lane in two stores, every 32-byte sector was written in halves: 150 us where this
+// takes READ32K_US, 4 sequences of 32K keys).
 __global__ void __launch_bounds__(kReadThreads) read_kv8_kernel(ReadArgs a) {
   const int b = blockIdx.z, g = blockIdx.y, tid = threadIdx.x;
   int n = a.n[b];
@@ -211,31 +260,48 @@ __global__ void __launch_bounds__(kReadThreads) read_kv8_kernel(ReadArgs a) {
     if (tid == 0 && blockIdx.x == 0 && g == 0) flag_status(kStatusClipped);
     n = a.max_n;
   }
-  const int i = blockIdx.x * kReadRows + (tid >> 3), lane = tid & 7;
-  if (i >= n) return;
-  const long long t = (long long)a.start[b] + i;
-  const long long lp = t / a.P;
-  if (t < 0 || lp >= a.maxp) {
-    if (lane == 0) flag_status(kStatusBadToken);
-    return;
+  const int i0 = blockIdx.x * kReadTile + (tid >> 4), lane = tid & 15;
+  if (i0 >= n) return;
+  const long long start = a.start[b];
+  constexpr int U = kReadUnroll;
+  constexpr uint32_t kNone = 0xffffffffu;
+  uint32_t row[U];  // cache row, or kNone
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int i = i0 + u * kReadRows;
+    const long long t = start + i;
+    row[u] = kNone;
+    if (i >= n) continue;
+    if (t < 0 || t >= a.maxp * a.P) {
+      if (lane == 0) flag_status(kStatusBadToken);
+      continue;
+    }
+    // t / P: t < 2^23 and P <= 256, so the error of the product is below 1 / P.
+    const int lp = a.P == 1 ? (int)t : (int)__umulhi((uint32_t)t, a.p_mul);
+    const int phys = a.page_table[(size_t)b * a.maxp + lp];
+    if (phys < 0 || phys >= a.n_phys) {
+      if (lane == 0) flag_status(kStatusBadPage);
+      continue;
+    }
+    row[u] = ((uint32_t)phys * (uint32_t)a.G + g) * (uint32_t)a.P + (uint32_t)((int)t - lp * a.P);
   }
-  const int phys = a.page_table[(size_t)b * a.maxp + lp];
-  if (phys < 0 || phys >= a.n_phys) {
-    if (lane == 0) flag_status(kStatusBadPage);
-    return;
+  uint2 q[2][U];
+  uint32_t x[2][U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (row[u] == kNone) continue;
+    q[0][u] = *reinterpret_cast<const uint2*>(a.k + (size_t)row[u] * kD + 8 * lane);
+    q[1][u] = *reinterpret_cast<const uint2*>(a.v + (size_t)row[u] * kD + 8 * lane);
+    x[0][u] = a.k_exp[row[u]];
+    x[1][u] = a.v_exp[row[u]];
   }
-  const size_t row = ((size_t)phys * a.G + g) * a.P + (size_t)(t - lp * a.P);
-  const uint4 kq = *reinterpret_cast<const uint4*>(a.k + row * kD + 16 * lane);
-  const uint4 vq = *reinterpret_cast<const uint4*>(a.v + row * kD + 16 * lane);
-  const uint32_t kx = a.k_exp[row], vx = a.v_exp[row];
-  const size_t o = (((size_t)b * a.max_n + i) * a.G + g) * kD + 16 * lane;
-  uint4 lo, hi;
-  dequantise16(kq, kx, lo, hi);
-  reinterpret_cast<uint4*>(a.k_out + o)[0] = lo;
-  reinterpret_cast<uint4*>(a.k_out + o)[1] = hi;
-  dequantise16(vq, vx, lo, hi);
-  reinterpret_cast<uint4*>(a.v_out + o)[0] = lo;
-  reinterpret_cast<uint4*>(a.v_out + o)[1] = hi;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (row[u] == kNone) continue;
+    const size_t o = (((size_t)b * a.max_n + (i0 + u * kReadRows)) * a.G + g) * kD + 8 * lane;
+    *reinterpret_cast<uint4*>(a.k_out + o) = dequantise8(q[0][u], x[0][u]);
+    *reinterpret_cast<uint4*>(a.v_out + o) = dequantise8(q[1][u], x[1][u]);
+  }
 }
 
 }  // namespace hhr
