@@ -66,12 +66,17 @@ __device__ __forceinline__ double shfl_xor_f64(double v, int o) {
   return __hiloint2double(__shfl_xor_sync(kFull, __double2hiint(v), o),
                           __shfl_xor_sync(kFull, __double2loint(v), o));
 }
-// Four channels of a row's query, summed over its gs <= 8 heads (all loads at once).
+// Four channels of a row's query over its gs <= NH heads, loaded at once: absent heads are read
+// as the last one (a conditional load would keep the next one waiting) and not used.
+template <int NH>
+__device__ __forceinline__ void bs_heads(const uint16_t* q, int gs, uint2 (&w)[NH]) {
+#pragma unroll
+  for (int h = 0; h < NH; ++h) w[h] = *reinterpret_cast<const uint2*>(q + (size_t)min(h, gs - 1) * kD);
+}
+// Their sums, in 64 bits (exact but for the last of 53) and in fp32.
 __device__ __forceinline__ void bs_query_sum(const uint16_t* q, int gs, double (&s)[4]) {
   uint2 w[kMaxGroup];
-#pragma unroll
-  for (int h = 0; h < kMaxGroup; ++h)
-    w[h] = h < gs ? *reinterpret_cast<const uint2*>(q + (size_t)h * kD) : make_uint2(0u, 0u);
+  bs_heads<kMaxGroup>(q, gs, w);
   s[0] = s[1] = s[2] = s[3] = 0.0;
 #pragma unroll
   for (int h = 0; h < kMaxGroup; ++h) {
@@ -81,24 +86,20 @@ __device__ __forceinline__ void bs_query_sum(const uint16_t* q, int gs, double (
     }
   }
 }
-// A score as it is kept; + 0 so that -0 ties with +0.
-__device__ __forceinline__ float bs_round(double s) { return (float)s + 0.f; }
-// The same sum in fp32.
+template <int NH>
 __device__ __forceinline__ float4 bs_query_sum_f32(const uint16_t* q, int gs) {
-  uint2 w[kMaxGroup];
-#pragma unroll
-  for (int h = 0; h < kMaxGroup; ++h)
-    w[h] = h < gs ? *reinterpret_cast<const uint2*>(q + (size_t)h * kD) : make_uint2(0u, 0u);
+  uint2 w[NH];
+  bs_heads<NH>(q, gs, w);
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-  for (int h = 0; h < kMaxGroup; ++h) {
-    if (h < gs) {
-      const float4 f = bf16x4_to_f4(w[h]);
-      s.x += f.x; s.y += f.y; s.z += f.z; s.w += f.w;
-    }
+  for (int h = 0; h < NH; ++h) {
+    const float4 f = bf16x4_to_f4(h < gs ? w[h] : make_uint2(0u, 0u));
+    s.x += f.x; s.y += f.y; s.z += f.z; s.w += f.w;
   }
   return s;
 }
+// A score as it is kept; + 0 so that -0 ties with +0.
+__device__ __forceinline__ float bs_round(double s) { return (float)s + 0.f; }
 // The definition's score of block p with a row's query sums (channels 4 lane + {0..3}); a warp.
 __device__ __forceinline__ float bs_exact(const BlockSelectArgs& a, int b, int g, int p,
                                           const double (&q)[4], int lane) {
@@ -181,7 +182,7 @@ __global__ void __launch_bounds__(kBvWarps * 32, kBvCtasPerSm)
     for (int i = tid; i < a.G * (kD / 4); i += kBvWarps * 32) {
       const int g = i / (kD / 4), c = i % (kD / 4);
       reinterpret_cast<float4*>(bv_q)[i] =
-          bs_query_sum_f32(bs_query(a, b, g, 0) + 4 * c, a.Hq / a.Gs);
+          bs_query_sum_f32<kMaxGroup>(bs_query(a, b, g, 0) + 4 * c, a.Hq / a.Gs);
     }
     __syncthreads();
     for (; i0 < end; i0 += kStep) {
@@ -243,6 +244,7 @@ __global__ void __launch_bounds__(kBvWarps * 32, kBvCtasPerSm)
 constexpr int kBtPages = 32, kBtRows = 32, kBtThreads = 128;
 constexpr int kBtStride = kD + 4;  // 16-byte rows, 4 banks apart
 inline size_t block_tile_smem() { return (size_t)(kBtPages + kBtRows) * kBtStride * 4; }
+template <int NH>
 __global__ void __launch_bounds__(kBtThreads, 4) block_mean_tile_kernel(BlockSelectArgs a) {
   extern __shared__ __align__(16) float bt_smem[];
   float* ms = bt_smem;                         // [kBtPages][kBtStride]
@@ -255,38 +257,56 @@ __global__ void __launch_bounds__(kBtThreads, 4) block_mean_tile_kernel(BlockSel
   const int n_b = bs_blocks(a, b);
   if (p0 >= n_b) return;
   const int rows = min(kBtRows, a.T * a.kv_div - r0);
-  // Warp w stages the blocks and the rows w, w + NW, ...; a lane 4 channels.
-#pragma unroll 4
-  for (int r = warp; r < kBtRows; r += NW)
-    *reinterpret_cast<float4*>(qs + r * kBtStride + 4 * lane) =
-        r < rows ? bs_query_sum_f32(bs_query(a, b, g, r0 + r) + 4 * lane, a.Hq / a.Gs)
-                 : make_float4(0.f, 0.f, 0.f, 0.f);
+  // Warp w stages the blocks and the rows w, w + NW, ...; a lane 4 channels. All loads are
+  // unconditional (blocks and rows past the end: the last one, not used).
   {
-    constexpr int N = kBtPages / NW;
-    int phys[N];
+    constexpr int N = kBtPages / NW, R = kBtRows / NW;
+    int page[N];
     float4 f[N];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int p = p0 + warp + i * NW;
-      phys[i] = p < n_b ? bs_page(a, b, p) : -1;
-    }
+    for (int i = 0; i < N; ++i)
+      page[i] = a.page_table[(size_t)b * a.maxp + min(p0 + warp + i * NW, n_b - 1)];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float x = __int_as_float(0x7fffffff);
-      f[i] = phys[i] >= 0 ? ldg_f4_now(reinterpret_cast<const float4*>(
-                                a.block_mean + ((size_t)phys[i] * a.G + g) * kD) + lane)
-                          : make_float4(x, x, x, x);
-    }
+    for (int i = 0; i < R; i += 2) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int p = warp + i * NW;
-      *reinterpret_cast<float4*>(ms + p * kBtStride + 4 * lane) = f[i];
-      if (r0 == 0) {
-        const float u = warp_sum(fmaf(f[i].x, f[i].x, f[i].y * f[i].y) +
-                                 fmaf(f[i].z, f[i].z, f[i].w * f[i].w));
-        if (lane == 0 && p0 + p < n_b) a.norms[((size_t)b * a.G + g) * a.maxp + p0 + p] = u;
+      for (int j = i; j < i + 2; ++j) {
+        const int r = warp + j * NW;
+        *reinterpret_cast<float4*>(qs + r * kBtStride + 4 * lane) =
+            bs_query_sum_f32<NH>(bs_query(a, b, g, r0 + min(r, rows - 1)) + 4 * lane, a.Hq / a.Gs);
       }
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const bool held = page[i] >= 0 && page[i] < a.n_phys;
+      f[i] = ldg_f4_now(reinterpret_cast<const float4*>(
+                            a.block_mean + ((size_t)(held ? page[i] : 0) * a.G + g) * kD) + lane);
+    }
+    float u[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (page[i] < 0 || page[i] >= a.n_phys) {
+        if (lane == 0) flag_status(kStatusBadPage);
+        f[i].x = __int_as_float(0x7fffffff);  // its score is NaN: it is never chosen
+      }
+      *reinterpret_cast<float4*>(ms + (warp + i * NW) * kBtStride + 4 * lane) = f[i];
+      u[i] = fmaf(f[i].x, f[i].x, f[i].y * f[i].y) + fmaf(f[i].z, f[i].z, f[i].w * f[i].w);
+    }
+    if (r0 == 0) {  // the means' norms, once: lane 4 i .. 4 i + 3 end with block i's
+#pragma unroll
+      for (int o = 16, w = N / 2; w >= 1; o >>= 1, w >>= 1) {
+        const bool upper = (lane & o) != 0;
+#pragma unroll
+        for (int k = 0; k < w; ++k) {
+          const float send = upper ? u[k] : u[k + w], keep = upper ? u[k + w] : u[k];
+          u[k] = keep + __shfl_xor_sync(kFull, send, o);
+        }
+      }
+      u[0] += __shfl_xor_sync(kFull, u[0], 2);
+      u[0] += __shfl_xor_sync(kFull, u[0], 1);
+      const int p = p0 + warp + (lane >> 2) * NW;
+      if ((lane & 3) == 0 && p < n_b) a.norms[((size_t)b * a.G + g) * a.maxp + p] = u[0];
+    }
+    static_assert(N == 8 && R % 2 == 0, "8 blocks per warp");
   }
   __syncthreads();
   // Threads 16 x 8: blocks tx + 16 i, rows ty + 8 j.

@@ -1017,12 +1017,11 @@ size_t page_ws(const hhr_dims* d, int n_ctas) {
 #endif
 int page_cluster(const hhr_dims* d, int T, int blocks, bool list) {
   const long long rows = (long long)d->batch * T * sel_rows(d);
-  const long long keys = (long long)blocks * d->page_size, n = (long long)kPaCtasPerSm * sm_count();
+  const long long keys = (long long)blocks * d->page_size, n = (long long)kPcCtasPerSm * sm_count();
   if (rows > n || (list && !HHR_PA_LIST_CLUSTER)) return 0;
   if (!list && keys > (d->batch == 1 ? HHR_PA_DENSE_CLUSTER1 : HHR_PA_DENSE_CLUSTER)) return 0;
-  int cs = kPaMaxCluster;
-  while (cs > 1 && (rows * cs > n || (long long)(cs / 2) * kUnitKeys >= keys)) cs /= 2;
-  return cs;
+  // As many as fit at once, and no more than the row has units.
+  return (int)max(1LL, min((long long)kPaMaxCluster, min(n / rows, (keys + kUnitKeys - 1) / kUnitKeys)));
 }
 
 // Launches the page attention and, where CTAs can share a row, the join of its partials.
@@ -1045,12 +1044,12 @@ int launch_page_attn(const hhr_dims* d, PageAttnArgs& a, bool k8, long long unit
     void (*kc)(PageAttnArgs) =
         k8 ? (pair ? page_cluster_kernel<true, kList, true> : page_cluster_kernel<true, kList, false>)
            : (pair ? page_cluster_kernel<false, kList, true> : page_cluster_kernel<false, kList, false>);
-    if (allow_smem(kc, page_attn_smem(), g_smem_cluster[k8][kList][pair]) != cudaSuccess)
+    if (allow_smem(kc, page_cluster_smem(), g_smem_cluster[k8][kList][pair]) != cudaSuccess)
       return HHR_ERR_CUDA;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.B * a.T * a.Gs * cs));
     cfg.blockDim = dim3(kPaThreads);
-    cfg.dynamicSmemBytes = page_attn_smem();
+    cfg.dynamicSmemBytes = page_cluster_smem();
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1259,7 +1258,7 @@ int hhr_block_select(const hhr_dims* d, int n_queries, const uint16_t* q, const 
     block_mean_stream_kernel<<<(unsigned)stream_ctas, kBvWarps * 32,
                                block_stream_smem(d->n_kv_heads), s>>>(a);
   else
-    block_mean_tile_kernel<<<dim3((maxp + kBtPages - 1) / kBtPages, (unsigned)tiles, B), kBtThreads,
+    (d->n_q_heads / Gs <= 4 ? block_mean_tile_kernel<4> : block_mean_tile_kernel<8>)<<<dim3((maxp + kBtPages - 1) / kBtPages, (unsigned)tiles, B), kBtThreads,
                              block_tile_smem(), s>>>(a);
   prof_end(HHR_KERNEL_MEAN, s);
   if ((st = launch_status()) != HHR_OK) return st;

@@ -108,6 +108,9 @@ __device__ __forceinline__ UnitPlace dense_place(const PageAttnArgs& a, int* sh,
 __device__ __forceinline__ void cp_async16_at(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void prefetch_l1(const void* p) {
+  asm volatile("prefetch.global.L1 [%0];\n" ::"l"(p) : "memory");
+}
 // 4 bytes into shared memory, of which the first n are read and the others are zeros.
 __device__ __forceinline__ void cp_async4_zfill(uint32_t dst, const void* src, uint32_t n) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(n)
@@ -205,7 +208,7 @@ __device__ __forceinline__ uint32_t row_of(const PageAttnArgs& a, const RowKeys&
   return ((uint32_t)page * (uint32_t)a.G + r.g) * (uint32_t)a.P + (uint32_t)slot;
 }
 
-// Shared memory of one warp: kPaStages stages of a K tile and a V tile, S rows each (16 bf16 or
+// Shared memory of one warp: NS stages of a K tile and a V tile, S rows each (16 bf16 or
 // 32 8-bit rows: 4 KB a tile). The 16-byte chunks of a row are XOR-swizzled by row % 8, so that
 // ldmatrix reads of 8 rows hit 8 distinct bank groups.
 // Beside the tiles lie, for an 8-bit cache, the aligned words that hold the rows' exponent bytes
@@ -213,12 +216,11 @@ __device__ __forceinline__ uint32_t row_of(const PageAttnArgs& a, const RowKeys&
 // step.
 constexpr int kPaTile = 4096;
 constexpr int kPaStage = 2 * kPaTile + 256;
-constexpr int kPaRing = kPaStages * kPaStage;
 
 // Keys [k0, k1) of a row, over the CTA's warps: the state of every head is left in shared
 // memory (mo [warps][8][d], ml [warps][8][2], which reuse the rings). Ends with the state of
 // all warps written (a barrier).
-template <bool K8, bool kList, bool kPair>
+template <bool K8, bool kList, bool kPair, int NS>
 __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKeys& rk,
                                              const uint16_t* q, int gs, int k0, int k1,
                                              char* smem, float* mo, float* ml) {
@@ -226,12 +228,11 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
   constexpr int NM = S / 16;            // 16-key tiles of S^T
   constexpr int RB = K8 ? kD : 2 * kD;  // bytes of a cache row
   constexpr int RC = RB / 16;           // 16-byte chunks of a row
-  constexpr int NS = kPaStages;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int gq = lane >> 2, tq = lane & 3;
   const char* kb = reinterpret_cast<const char*>(a.k);
   const char* vb = reinterpret_cast<const char*>(a.v);
-  const uint32_t ring = smem_u32(smem) + (uint32_t)warp * kPaRing;
+  const uint32_t ring = smem_u32(smem) + (uint32_t)warp * (NS * kPaStage);
   const int base = k0 + warp * S, stride = kPaWarps * S;
   const int lk = K8 ? lane : (lane & 15);  // the key of a step that this lane locates
 
@@ -533,10 +534,25 @@ __device__ __forceinline__ void put_out(const PageAttnArgs& a, size_t head, int 
 }
 
 // The rings; the warps' states lie over them.
-constexpr int kPaMaxCluster = 8;
-inline size_t page_attn_smem() { return (size_t)kPaWarps * kPaRing; }
-static_assert((kPaWarps + 1) * kMaxGroup * (kD + 2) * 4 <= kPaWarps * kPaRing,
-              "the warps' states and the CTA's fit the rings");
+inline size_t page_attn_smem() { return (size_t)kPaWarps * kPaStages * kPaStage; }
+static_assert(kMaxGroup * (kD + 2) * 4 <= kPaStages * kPaStage, "a warp's state fits its ring");
+
+// Clusters: beside the rings lies what the ranks send one another: the ranks' shares of a rank's
+// outputs (at most kMaxGroup d, rounded up per rank), then per rank and head (maximum, sum).
+// Three stages at two CTAs per SM are no faster (8 sequences x 64 pages: 14.3 us either way; 48
+// queries x 16 pages: 24.7 us against 18.4 us).
+#ifndef HHR_PC_STAGES
+#define HHR_PC_STAGES 2
+#endif
+#ifndef HHR_PC_CTAS
+#define HHR_PC_CTAS 3
+#endif
+constexpr int kPcStages = HHR_PC_STAGES, kPcCtasPerSm = HHR_PC_CTAS, kPaMaxCluster = 8;
+constexpr int kPcShares = kMaxGroup * kD + kPaMaxCluster;                          // floats
+constexpr int kPcInbox = kPcShares + 2 * kPaMaxCluster * kMaxGroup;
+inline size_t page_cluster_smem() {
+  return (size_t)kPaWarps * kPcStages * kPaStage + (size_t)kPcInbox * 4;
+}
 
 // Row `row` (over all sequences and tokens), sequence b: where its keys are.
 template <bool kList>
@@ -633,7 +649,7 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
     if (!kList && a.k_new != nullptr && off + take == ub && rk.n > 0) append_row<K8>(a, rk, b);
     __syncthreads();  // the new row is visible; the previous segment's state has been read
     const size_t head0 = (size_t)bt * a.Hq + (size_t)r * gs;
-    page_segment<K8, kList, kPair>(a, rk, a.q + head0 * kD, gs, off * kUnitKeys,
+    page_segment<K8, kList, kPair, kPaStages>(a, rk, a.q + head0 * kD, gs, off * kUnitKeys,
                             min(rk.n, (off + take) * kUnitKeys),
                             reinterpret_cast<char*>(pa_smem), mo, ml);
     const bool whole = off == 0 && take == ub;
@@ -663,20 +679,29 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
   }
 }
 
-// One cluster per row: its CTAs take equal parts of the row's keys and are joined through
-// distributed shared memory, each rank writing its share of the row's outputs. One launch, and no
-// partials in global memory.
+// One cluster per row: its CTAs take equal parts of the row's keys. Rank r writes the r-th part of
+// the row's outputs: every rank sends it that part of its state through distributed shared memory,
+// into an inbox beside the rings. One launch, no partials in global memory.
 template <bool K8, bool kList, bool kPair>
-__global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_cluster_kernel(PageAttnArgs a) {
+__global__ void __launch_bounds__(kPaThreads, kPcCtasPerSm) page_cluster_kernel(PageAttnArgs a) {
   namespace cg = cooperative_groups;
   extern __shared__ float4 pa_smem[];
+  cluster_arrive();  // waited for before the first remote write: every rank has started
   float* mo = reinterpret_cast<float*>(pa_smem);
   float* ml = mo + kPaWarps * kMaxGroup * kD;
-  float* res = ml + kPaWarps * kMaxGroup * 2;  // this CTA's state: [gs][d], then [gs][2]
   cg::cluster_group cl = cg::this_cluster();
   const int tid = threadIdx.x, gs = a.Hq / a.Gs;
   const int cs = (int)cl.num_blocks(), rank = (int)cl.block_rank(), row = blockIdx.x / cs;
   const int bt = row / a.Gs, r = row - bt * a.Gs, b = bt / a.T;
+  // Slot s of the inbox: rank s's share of this rank's outputs ([part]), and its (M, L) per head.
+  const int part = ceil_div(gs * kD, cs);
+  float* inbox = reinterpret_cast<float*>(reinterpret_cast<char*>(pa_smem) +
+                                          (size_t)kPaWarps * kPcStages * kPaStage);
+  float* inbox_ml = inbox + kPcShares;
+  // Where the keys lie takes three dependent loads (length, block or page id, key): the page ids
+  // and the block list are brought into L1 while the length is on its way.
+  if (32 * tid < a.maxp) prefetch_l1(a.page_table + (size_t)b * a.maxp + 32 * tid);
+  if (kList && 32 * tid < a.m_max) prefetch_l1(a.blocks + (size_t)row * a.m_max + 32 * tid);
   const RowKeys rk = row_keys<kList>(a, row, b);
   constexpr int kIter = kPaWarps * (K8 ? 32 : 16);  // keys of an iteration of the CTA
   const int per = ceil_div(ceil_div(rk.n, cs), kIter) * kIter;
@@ -684,44 +709,42 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_cluster_kernel(
   if (!kList && a.k_new != nullptr && k0 < k1 && k1 == rk.n) append_row<K8>(a, rk, b);
   __syncthreads();
   const size_t head0 = (size_t)bt * a.Hq + (size_t)r * gs;
-  page_segment<K8, kList, kPair>(a, rk, a.q + head0 * kD, gs, k0, k1, reinterpret_cast<char*>(pa_smem), mo,
-                          ml);
+  page_segment<K8, kList, kPair, kPcStages>(a, rk, a.q + head0 * kD, gs, k0, k1,
+                                            reinterpret_cast<char*>(pa_smem), mo, ml);
+  cluster_wait();
   for (int i = tid; i < gs * kD; i += kPaThreads) {
-    const int h = i / kD, ch = i % kD;
+    const int h = i / kD, to = i / part;
     float M, L, O;
-    join_warps(mo, ml, h, ch, M, L, O);
-    res[h * kD + ch] = O;
-    if (ch == 0) {
-      res[kMaxGroup * kD + 2 * h] = M;
-      res[kMaxGroup * kD + 2 * h + 1] = L;
+    join_warps(mo, ml, h, i % kD, M, L, O);
+    *cl.map_shared_rank(inbox + rank * part + (i - to * part), to) = O;
+    if (i % kD < cs) {  // (M, L) of the head, once to each rank
+      float* x = cl.map_shared_rank(inbox_ml + (rank * kMaxGroup + h) * 2, i % kD);
+      x[0] = M;
+      x[1] = L;
     }
   }
-  cluster_sync_all();  // every rank's state is in its shared memory
-  const int part = ceil_div(gs * kD, cs), i0 = rank * part, i1 = min(gs * kD, i0 + part);
-  for (int i = i0 + tid; i < i1; i += kPaThreads) {
-    const int h = i / kD, ch = i % kD;
-    float m[kPaMaxCluster], l[kPaMaxCluster], o[kPaMaxCluster];
+  cluster_sync_all();  // every rank's share has arrived; no remote access follows
+  const int n = min(part, gs * kD - rank * part);
+  for (int j = tid; j < n; j += kPaThreads) {
+    const int i = rank * part + j, h = i / kD;
+    float m[kPaMaxCluster], M = -INFINITY;
 #pragma unroll
     for (int c = 0; c < kPaMaxCluster; ++c) {
-      const float* x = cl.map_shared_rank(res, c < cs ? c : 0);
-      m[c] = c < cs ? x[kMaxGroup * kD + 2 * h] : -INFINITY;
-      l[c] = c < cs ? x[kMaxGroup * kD + 2 * h + 1] : 0.f;
-      o[c] = c < cs ? x[h * kD + ch] : 0.f;
+      m[c] = c < cs ? inbox_ml[(c * kMaxGroup + h) * 2] : -INFINITY;
+      M = fmaxf(M, m[c]);
     }
-    float M = -INFINITY;
-#pragma unroll
-    for (int c = 0; c < kPaMaxCluster; ++c) M = fmaxf(M, m[c]);
     const float mu = M == -INFINITY ? 0.f : M;
     float L = 0.f, O = 0.f;
 #pragma unroll
     for (int c = 0; c < kPaMaxCluster; ++c) {
-      const float f = exp2f(m[c] - mu);
-      L = fmaf(f, l[c], L);
-      O = fmaf(f, o[c], O);
+      if (c < cs) {
+        const float f = exp2f(m[c] - mu);
+        L = fmaf(f, inbox_ml[(c * kMaxGroup + h) * 2 + 1], L);
+        O = fmaf(f, inbox[c * part + j], O);
+      }
     }
-    put_out(a, head0 + h, ch, M, L, O);
+    put_out(a, head0 + h, i % kD, M, L, O);
   }
-  cluster_sync_all();  // no CTA leaves while its shared memory is read
 }
 
 // Joins the partials of one row and head: the CTAs c0..c1 whose shares touch the row, the first
