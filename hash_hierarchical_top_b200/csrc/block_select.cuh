@@ -141,6 +141,7 @@ __global__ void __launch_bounds__(kBvWarps * 32, kBvCtasPerSm)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int lg = lane >> 3, lc = lane & 7;  // row of a step, channel part
   constexpr int NK = kBvItem / 4;
+  pdl_wait();
   pdl_trigger();
   const UnitPlace at = place_units(a.B, sh, [&](int b) { return bs_blocks(a, b); }, [&](int all) {
     return all == 0 ? -1 : min(share_begin(blockIdx.x, all, gridDim.x), all - 1);
@@ -253,6 +254,7 @@ __global__ void __launch_bounds__(kBtThreads, 4) block_mean_tile_kernel(BlockSel
   const int g = blockIdx.y % a.G, r0 = (blockIdx.y / a.G) * kBtRows;
   const int lane = tid & 31, warp = tid >> 5;
   constexpr int NW = kBtThreads / 32;
+  pdl_wait();
   pdl_trigger();
   const int n_b = bs_blocks(a, b);
   if (p0 >= n_b) return;

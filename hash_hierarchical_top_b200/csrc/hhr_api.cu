@@ -1002,6 +1002,38 @@ size_t page_ws(const hhr_dims* d, int n_ctas) {
   return align256((size_t)2 * n_ctas * gs * kD * 4) + align256((size_t)2 * n_ctas * gs * 2 * 4);
 }
 
+// Launches a call's first kernel, behind whatever the stream holds, with programmatic stream
+// serialisation: its CTAs are placed while the kernel before them drains, and wait
+// (griddepcontrol.wait, their first instruction) until it has completed. Measured on calls in a
+// row: 517 keys dense 8.2 -> 5.8 us, reading 700 keys back 4.1 -> 2.9 us.
+template <typename Args>
+int launch_first(int prof, void (*kernel)(Args), dim3 grid, int threads, size_t smem,
+                 cudaStream_t s, const Args& args, int cluster = 1) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  prof_begin(prof, s);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
+  prof_end(prof, s);
+  if (e != cudaSuccess) {
+    g_last_cuda = e;
+    cudaGetLastError();
+    return HHR_ERR_CUDA;
+  }
+  return HHR_OK;
+}
+
 // CTAs of the cluster that takes one row, or 0 for even shares of all rows' keys with a join.
 // Clusters need one launch and no join, but split every row alike: they are taken where all rows'
 // clusters are resident at once, for lists (rows of one capacity), and for dense rows of up to
@@ -1046,32 +1078,15 @@ int launch_page_attn(const hhr_dims* d, PageAttnArgs& a, bool k8, long long unit
            : (pair ? page_cluster_kernel<false, kList, true> : page_cluster_kernel<false, kList, false>);
     if (allow_smem(kc, page_cluster_smem(), g_smem_cluster[k8][kList][pair]) != cudaSuccess)
       return HHR_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(a.B * a.T * a.Gs * cs));
-    cfg.blockDim = dim3(kPaThreads);
-    cfg.dynamicSmemBytes = page_cluster_smem();
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = cs;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    prof_begin(HHR_KERNEL_PAGE, s);
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kc, a);
-    prof_end(HHR_KERNEL_PAGE, s);
-    if (e != cudaSuccess) { g_last_cuda = e; return HHR_ERR_CUDA; }
-    return HHR_OK;
+    return launch_first(HHR_KERNEL_PAGE, kc, dim3((unsigned)(a.B * a.T * a.Gs * cs)), kPaThreads,
+                        page_cluster_smem(), s, a, cs);
   }
   void (*k)(PageAttnArgs) =
       k8 ? (pair ? page_attn_kernel<true, kList, true> : page_attn_kernel<true, kList, false>)
          : (pair ? page_attn_kernel<false, kList, true> : page_attn_kernel<false, kList, false>);
   if (allow_smem(k, page_attn_smem(), g_smem_page[k8][kList][pair]) != cudaSuccess) return HHR_ERR_CUDA;
-  prof_begin(HHR_KERNEL_PAGE, s);
-  k<<<a.n_ctas, kPaThreads, page_attn_smem(), s>>>(a);
-  prof_end(HHR_KERNEL_PAGE, s);
-  int st = launch_status();
+  const int st = launch_first(HHR_KERNEL_PAGE, k, dim3((unsigned)a.n_ctas), kPaThreads,
+                              page_attn_smem(), s, a);
   if (st != HHR_OK) return st;
   prof_begin(HHR_KERNEL_JOIN, s);
   const cudaError_t e = launch_pdl(page_join_kernel<kList>, dim3((unsigned)(a.B * a.T * a.Gs), (unsigned)gs),
@@ -1147,13 +1162,9 @@ int hhr_append_kv8(const hhr_dims* d, const uint16_t* k_new, const uint16_t* v_n
                max_new};
   const dim3 grid((unsigned)pages, d->n_kv_heads, d->batch);
   cudaStream_t s = (cudaStream_t)stream;
-  prof_begin(HHR_KERNEL_APPEND, s);
-  if (block_mean != nullptr)
-    append_kv8_kernel<true><<<grid, kAppendThreads, 0, s>>>(a);
-  else
-    append_kv8_kernel<false><<<grid, kAppendThreads, 0, s>>>(a);
-  prof_end(HHR_KERNEL_APPEND, s);
-  return launch_status();
+  return launch_first(HHR_KERNEL_APPEND,
+                      block_mean != nullptr ? append_kv8_kernel<true> : append_kv8_kernel<false>,
+                      grid, kAppendThreads, 0, s, a);
 }
 
 int hhr_read_kv8(const hhr_dims* d, const uint8_t* k, const uint8_t* v, const uint8_t* k_exp,
@@ -1170,12 +1181,10 @@ int hhr_read_kv8(const hhr_dims* d, const uint8_t* k, const uint8_t* v, const ui
   ReadArgs a{k, v, k_exp, v_exp, page_table, start, n, k_out, v_out, d->n_kv_heads, d->page_size,
              d->max_pages_per_seq, d->n_phys_pages, max_n, page_mul(d->page_size)};
   cudaStream_t s = (cudaStream_t)stream;
-  prof_begin(HHR_KERNEL_READ, s);
-  read_kv8_kernel<<<dim3((unsigned)((max_n + (long long)kReadTile - 1) / kReadTile),
-                         d->n_kv_heads, d->batch),
-                    kReadThreads, 0, s>>>(a);
-  prof_end(HHR_KERNEL_READ, s);
-  return launch_status();
+  return launch_first(HHR_KERNEL_READ, read_kv8_kernel,
+                      dim3((unsigned)((max_n + (long long)kReadTile - 1) / kReadTile),
+                           d->n_kv_heads, d->batch),
+                      kReadThreads, 0, s, a);
 }
 
 size_t hhr_paged_attn_workspace_bytes(const hhr_dims* d) {
@@ -1253,15 +1262,15 @@ int hhr_block_select(const hhr_dims* d, int n_queries, const uint16_t* q, const 
   void (*topm)(BlockSelectArgs) = wide ? block_topm_kernel<512> : block_topm_kernel<128>;
   if (smem > kDefaultSmem && allow_smem(topm, smem, g_smem_topm[wide]) != cudaSuccess)
     return HHR_ERR_CUDA;
-  prof_begin(HHR_KERNEL_MEAN, s);
   if (single)
-    block_mean_stream_kernel<<<(unsigned)stream_ctas, kBvWarps * 32,
-                               block_stream_smem(d->n_kv_heads), s>>>(a);
+    st = launch_first(HHR_KERNEL_MEAN, block_mean_stream_kernel, dim3((unsigned)stream_ctas),
+                      kBvWarps * 32, block_stream_smem(d->n_kv_heads), s, a);
   else
-    (d->n_q_heads / Gs <= 4 ? block_mean_tile_kernel<4> : block_mean_tile_kernel<8>)<<<dim3((maxp + kBtPages - 1) / kBtPages, (unsigned)tiles, B), kBtThreads,
-                             block_tile_smem(), s>>>(a);
-  prof_end(HHR_KERNEL_MEAN, s);
-  if ((st = launch_status()) != HHR_OK) return st;
+    st = launch_first(HHR_KERNEL_MEAN,
+                      d->n_q_heads / Gs <= 4 ? block_mean_tile_kernel<4> : block_mean_tile_kernel<8>,
+                      dim3((maxp + kBtPages - 1) / kBtPages, (unsigned)tiles, B), kBtThreads,
+                      block_tile_smem(), s, a);
+  if (st != HHR_OK) return st;
   prof_begin(HHR_KERNEL_TOPM, s);
   const cudaError_t e = launch_pdl(topm, dim3((unsigned)(B * n_queries * Gs)),
                                    dim3(wide ? 512 : 128), smem, s, a);

@@ -119,6 +119,8 @@ constexpr int kAppendUnroll = HHR_APPEND_UNROLL;
 // over the values that the cache stands for.
 template <bool kMean>
 __global__ void __launch_bounds__(kAppendThreads) append_kv8_kernel(AppendArgs a) {
+  pdl_wait();
+  pdl_trigger();
   __shared__ float part[kMean ? kAppendRows : 1][kD];
   const int b = blockIdx.z, g = blockIdx.y, tid = threadIdx.x;
   const int P = a.P;
@@ -254,6 +256,8 @@ __device__ __forceinline__ uint4 dequantise8(uint2 q, uint32_t x) {
 // (with 32 a lane in two stores, every 32-byte sector was written in halves: 150 us where this
 // takes READ32K_US, 4 sequences of 32K keys).
 __global__ void __launch_bounds__(kReadThreads) read_kv8_kernel(ReadArgs a) {
+  pdl_wait();
+  pdl_trigger();
   const int b = blockIdx.z, g = blockIdx.y, tid = threadIdx.x;
   int n = a.n[b];
   if (n > a.max_n) {

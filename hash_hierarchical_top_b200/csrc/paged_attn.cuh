@@ -610,6 +610,7 @@ __device__ __forceinline__ void join_warps(const float* mo, const float* ml, int
 // Even shares of all rows' keys (see the head of this file).
 template <bool K8, bool kList, bool kPair>
 __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(PageAttnArgs a) {
+  pdl_wait();
   extern __shared__ float4 pa_smem[];
   __shared__ int sh[40];
   float* mo = reinterpret_cast<float*>(pa_smem);
@@ -684,6 +685,8 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
 // into an inbox beside the rings. One launch, no partials in global memory.
 template <bool K8, bool kList, bool kPair>
 __global__ void __launch_bounds__(kPaThreads, kPcCtasPerSm) page_cluster_kernel(PageAttnArgs a) {
+  pdl_wait();
+  pdl_trigger();
   namespace cg = cooperative_groups;
   extern __shared__ float4 pa_smem[];
   cluster_arrive();  // waited for before the first remote write: every rank has started
@@ -777,6 +780,7 @@ __global__ void __launch_bounds__(kJoinThreads) page_join_kernel(PageAttnArgs a)
   const int n = min(a.n_ctas, total);
   const int c0 = share_of(first, total, n), parts = share_of(first + ub - 1, total, n) - c0 + 1;
   pdl_wait();
+  pdl_trigger();
   if (parts == 1) return;
   auto slot = [&](int i) { return ((size_t)2 * (c0 + i) + (i == 0 ? 1 : 0)) * gs + h; };
   float M = -INFINITY;
