@@ -22,8 +22,8 @@
 //     of O^T = V^T P^T (channels on M, heads on N) by one 8 x 8 transposition per 8 keys.
 //   - Page ids are loaded two steps ahead of the rows they locate, the rows one step ahead of
 //     their use.
-// P is used as two parts (hi + lo): bf16 parts leave 2^-17 of it, f16 parts 2^-22, so that the
-// fp32 output is not limited by the matrix operands' type.
+// P is used in parts (bf16: three, f16: two), so that the fp32 output is not limited by the matrix
+// operands' type.
 //
 // 8-bit cache: e4m3 numbers become f16 exactly. Q is scaled by a power of two per head so that
 // its largest channel is in [2^14, 2^15): bf16 queries are then exact in f16 down to 2^-38 of
@@ -153,16 +153,20 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
   return r;
 }
-// Two weights as hi + lo parts of the matrix operand's type.
+// Two weights as parts of the matrix operands' type: f16 hi + lo leave 2^-22 of a weight; bf16
+// takes a third part to leave 2^-27 (two leave 2^-18, which alone put the output 1.5e-6 off).
 template <bool K8>
-__device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo, uint32_t& lo2) {
   if constexpr (K8) {
     hi = pack_f16(x, y);
     const float2 h = f16x2_to_f2(hi);
     lo = pack_f16(x - h.x, y - h.y);
+    lo2 = 0u;
   } else {
     hi = pack_bf16(x, y);
-    lo = pack_bf16(x - bf16_lo(hi), y - bf16_hi(hi));
+    const float rx = x - bf16_lo(hi), ry = y - bf16_hi(hi);  // exact
+    lo = pack_bf16(rx, ry);
+    lo2 = pack_bf16(rx - bf16_lo(lo), ry - bf16_hi(lo));
   }
 }
 
@@ -429,8 +433,8 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
     }
     // Weights, as two parts of the operands' type, transposed into B operands: ph[i] holds the
     // keys 8i + 2tq, 8i + 2tq + 1 of column gq. kPair: columns 0-3 take the first parts, 4-7 the
-    // second, in one product.
-    uint32_t ph[2 * NM], pl[2 * NM];
+    // second, in one product. pm: the third parts (bf16).
+    uint32_t ph[2 * NM], pl[2 * NM], pm[2 * NM];
 #pragma unroll
     for (int m = 0; m < NM; ++m)
 #pragma unroll
@@ -442,8 +446,9 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
           l_run[e] += p[e];
           if constexpr (K8) p[e] *= __uint_as_float(ke[m][r] << 16);
         }
-        uint32_t hi, lo;
-        split_pair<K8>(p[0], p[1], hi, lo);
+        uint32_t hi, lo, lo2;
+        split_pair<K8>(p[0], p[1], hi, lo, lo2);
+        if constexpr (!K8) pm[2 * m + r] = movmatrix(kPair && tq >= 2 ? 0u : lo2);
         if constexpr (kPair) {
           ph[2 * m + r] = movmatrix(tq < 2 ? hi : lo);
         } else {
@@ -476,6 +481,7 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
         ldsm_x4_t(vs + (uint32_t)(r * RB + (((2 * i + (mj & 1)) ^ l8) << 4)), w[0], w[1], w[2], w[3]);
         mma_16816(o, w[0], w[1], w[2], w[3], ph[0], ph[1]);
         if constexpr (!kPair) mma_16816(o, w[0], w[1], w[2], w[3], pl[0], pl[1]);
+        mma_16816(o, w[0], w[1], w[2], w[3], pm[0], pm[1]);
       }
       oacc[i][0] = fmaf(oacc[i][0], corr[0], o[0]);
       oacc[i][1] = fmaf(oacc[i][1], corr[1], o[1]);

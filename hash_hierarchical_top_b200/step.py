@@ -3,7 +3,10 @@
 ``LayerCache`` holds the per-layer retrieval metadata (page summaries, codes,
 block means) next to the caller's K/V cache; ``DecodeStep`` owns the workspaces
 and outputs of one decode step and runs append-encode -> select -> sparse
-attention through the C ABI on one stream. PyTorch only allocates memory here;
+attention through the C ABI on one stream. ``KV8Cache`` is a layer's 8-bit K/V
+cache; ``DenseStep`` attends to every key of a cache (bf16 or 8-bit), and
+``BlockStep`` selects blocks by their mean keys and attends to those, for one
+token or a chunk of queries per sequence. PyTorch only allocates memory here;
 every step of the path runs in the library's kernels.
 """
 from __future__ import annotations
@@ -92,3 +95,102 @@ class DecodeStep:
         self.select(q, seq_len, page_table, cache, R=R, W=W, stream=stream)
         self.attend(q, k_cache, v_cache, page_table, seq_len, stream=stream)
         return self.out
+
+
+class KV8Cache:
+    """A layer's 8-bit K/V cache (e4m3 with one exponent byte per row), and optionally the mean
+    key of every page, laid out as include/hhr.h documents."""
+
+    def __init__(self, d: hhr.Dims, device, block_means=False):
+        shape = (d.n_phys_pages, d.n_kv_heads, d.page_size)
+        self.d = d
+        self.k, self.v = (torch.zeros(*shape, d.head_dim, dtype=torch.uint8, device=device)
+                          .view(torch.float8_e4m3fn) for _ in range(2))
+        self.k_exp, self.v_exp = (torch.zeros(shape, dtype=torch.uint8, device=device)
+                                  for _ in range(2))
+        self.block_mean = (torch.zeros(d.n_phys_pages, d.n_kv_heads, d.head_dim,
+                                       dtype=torch.float32, device=device)
+                           if block_means else None)
+
+    def append(self, k_new, v_new, start, n_new, page_table, stream=None):
+        """Quantise new rows [B][max_new][G][d] into positions [start, start + n_new)."""
+        hhr.hhr_append_kv8(self.d, k_new, v_new, start, n_new, page_table, self.k, self.v,
+                           self.k_exp, self.v_exp, self.block_mean, stream)
+
+    def read(self, start, n, page_table, k_out, v_out, stream=None):
+        """Read positions [start, start + n) back as bf16 [B][max_n][G][d]."""
+        hhr.hhr_read_kv8(self.d, self.k, self.v, self.k_exp, self.v_exp, page_table, start, n,
+                         k_out, v_out, stream)
+
+
+def _cache_args(cache):
+    """(k, v, k_exp, v_exp) of a KV8Cache, or of a (k_cache, v_cache) pair in bf16."""
+    if isinstance(cache, KV8Cache):
+        return cache.k, cache.v, cache.k_exp, cache.v_exp
+    k, v = cache
+    return k, v, None, None
+
+
+class DenseStep:
+    """Workspace and outputs of dense decode attention: one new token per sequence over every key
+    of its cache."""
+
+    def __init__(self, d: hhr.Dims, device, out_dtype=torch.float32):
+        self.d = d
+        n = hhr.hhr_paged_attn_workspace_bytes(d)
+        if n == 0:
+            raise ValueError("unsupported dims")
+        self.ws = torch.empty(n, dtype=torch.uint8, device=device)
+        self.out = torch.empty(d.batch, d.n_q_heads, d.head_dim, dtype=out_dtype, device=device)
+        self.lse = torch.empty(d.batch, d.n_q_heads, dtype=torch.float32, device=device)
+
+    def attend(self, q, cache, page_table, seq_len, k_new=None, v_new=None, scale=None,
+               stream=None):
+        """cache: a KV8Cache, or (k_cache, v_cache) in bf16. k_new, v_new [B][G][d]: the rows of
+        position seq_len - 1, written by the same call."""
+        if scale is None:
+            scale = 1.0 / math.sqrt(self.d.head_dim)
+        k, v, k_exp, v_exp = _cache_args(cache)
+        hhr.hhr_paged_attn(self.d, q, k_new, v_new, k, v, k_exp, v_exp, page_table, seq_len, scale,
+                           self.out, self.ws, self.lse, stream)
+        return self.out
+
+
+class BlockStep:
+    """Workspaces, block lists and outputs of block-sparse attention for n_queries tokens per
+    sequence."""
+
+    def __init__(self, d: hhr.Dims, n_queries: int, m_pages: int, device, sink_pages: int = 0,
+                 local_pages: int = 0, out_dtype=torch.float32):
+        self.d, self.m_pages = d, m_pages
+        self.opts = hhr.make_opts(sink_pages, local_pages)
+        m_max = hhr.hhr_kept_max(d, m_pages, 0)
+        sel = hhr.hhr_block_select_workspace_bytes(d, n_queries)
+        att = hhr.hhr_block_attn_workspace_bytes(d, n_queries, m_max)
+        if m_max < 1 or sel == 0 or att == 0:
+            raise ValueError("unsupported block selection parameters")
+        u8 = dict(dtype=torch.uint8, device=device)
+        self.sel_ws, self.attn_ws = torch.empty(sel, **u8), torch.empty(att, **u8)
+        B, T, rows = d.batch, n_queries, hhr.sel_rows(d)
+        self.blocks = torch.empty(B, T, rows, m_max, dtype=torch.int32, device=device)
+        self.count = torch.empty(B, T, rows, dtype=torch.int32, device=device)
+        self.out = torch.empty(B, T, d.n_q_heads, d.head_dim, dtype=out_dtype, device=device)
+        self.lse = torch.empty(B, T, d.n_q_heads, dtype=torch.float32, device=device)
+
+    def select(self, q, seq_len, page_table, block_mean, q_pos=None, stream=None):
+        hhr.hhr_block_select(self.d, q, seq_len, q_pos, page_table, block_mean, self.m_pages,
+                             self.blocks, self.count, self.sel_ws, stream, self.opts)
+
+    def attend(self, q, cache, page_table, seq_len, q_pos=None, scale=None, stream=None):
+        if scale is None:
+            scale = 1.0 / math.sqrt(self.d.head_dim)
+        k, v, k_exp, v_exp = _cache_args(cache)
+        hhr.hhr_block_attn(self.d, q, k, v, k_exp, v_exp, page_table, seq_len, q_pos, self.blocks,
+                           self.count, scale, self.out, self.attn_ws, self.lse, stream)
+        return self.out
+
+    def step(self, q, cache, page_table, seq_len, block_mean=None, q_pos=None, stream=None):
+        """Select by block_mean (a KV8Cache's own when None), then attend."""
+        mean = cache.block_mean if block_mean is None else block_mean
+        self.select(q, seq_len, page_table, mean, q_pos, stream)
+        return self.attend(q, cache, page_table, seq_len, q_pos, stream=stream)

@@ -7,10 +7,10 @@ Tolerances, per output channel, for rows of n keys (all of them worst cases adde
     the logit itself, 2^-22 |s| (scale, log2 e, exponent, difference to the maximum); ds = the
     largest of these over the row. A weight exp(s - max) is then off by ds, relative, and the
     weights' sum by as much again;
-  * a weight as two operand parts: 2^-16 (bf16: 2^-8 of a remainder of 2^-8);
+  * a weight as operand parts: 2^-21 (f16: 2^-11 of a remainder of 2^-11; bf16 parts leave less);
   * sums of n weights and n weighted values, 16 or 32 keys a step over at least 8 warps:
     (n / 128 + 64) 2^-22 of the sum of magnitudes (the 64: joins of warps and of splits, exp2);
-  so |o - o_ref| <= (2 ds + 2^-16 + (n / 128 + 64) 2^-22) sum_j w_j |v_jc|, plus 2^-8 |o_ref| for
+  so |o - o_ref| <= (2 ds + 2^-21 + (n / 128 + 64) 2^-22) sum_j w_j |v_jc|, plus 2^-8 |o_ref| for
   a bf16 output, and |lse - lse_ref| <= ds + (n / 128 + 64) 2^-22 + 2^-22 |lse_ref|.
 """
 from __future__ import annotations
@@ -131,7 +131,7 @@ def attend_ref(q, k, v, scale):
     o, mag = (w @ v) / total, (w @ v.abs()) / total
     lse = (top + total.log())[:, 0]
     sums = (n / 128 + 64) * 2.0 ** -22
-    return o, lse, (2 * ds[:, None] + 2.0 ** -16 + sums) * mag, ds + sums + 2.0 ** -22 * lse.abs()
+    return o, lse, (2 * ds[:, None] + 2.0 ** -21 + sums) * mag, ds + sums + 2.0 ** -22 * lse.abs()
 
 
 def check(got, ref, tol, what):

@@ -111,6 +111,85 @@ def test_ties_zeros_and_non_finite_scores():
     assert ask(4, hhr.make_opts(2, 1)) == [0, 1, 30, 39]
 
 
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("kind", ["levels", "equal", "huge", "tiny", "mixed", "close"])
+def test_many_ties_and_extreme_sizes(kind, T):
+    """Scores that crowd at the cut: few distinct means, equal ones, sizes past what fp32 squares
+    hold, blocks of very different sizes, and scores that differ in the last bits only."""
+    build.build()
+    P, n, G, m = 16, 2500, 2, 100
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    means = torch.randn(n + 1, G, D, generator=gen, device="cuda")
+    if kind == "levels":
+        means = means[torch.randint(0, 9, (n + 1,), generator=gen, device="cuda")].clone()
+    elif kind == "equal":
+        means = means[:1].expand(n + 1, G, D).contiguous()
+    elif kind == "huge":
+        means *= 1e25
+    elif kind == "tiny":
+        means *= 1e-25
+    elif kind == "mixed":
+        means *= torch.exp2(torch.randint(-60, 30, (n + 1, 1, 1), generator=gen, device="cuda").float())
+    else:
+        means = means[:1] * (1 + 1e-6 * torch.randn(n + 1, G, 1, generator=gen, device="cuda"))
+    means = means.contiguous()
+    d = hhr.make_dims(2, 4, G, P, n, n + 1)
+    pt = torch.stack([torch.randperm(n + 1, generator=gen, device="cuda")[:n] for _ in "ab"]).int()
+    lens = [n * P, 2000 * P - 3]
+    q = torch.randn(2, T, 4, D, generator=gen, device="cuda").bfloat16()
+    seq_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for opts in (None, hhr.make_opts(3, 2)):
+        blocks, count = select(d, q, seq_len, None, pt, means, m, opts)
+        status_ok()
+        ref = reference(q, means, pt, lens, None, P, G, m, *((3, 2) if opts else (0, 0)))
+        assert torch.equal(count.cpu(), ref[1]) and torch.equal(blocks.cpu(), ref[0])
+
+
+def test_long_rows_and_captured_calls():
+    """32768 blocks a sequence (keys past the narrow and the wide choice's registers), and the
+    call captured once and replayed on other inputs."""
+    build.build()
+    P, n, G, m = 4, 32768, 1, 2000
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    means = torch.randn(n, G, D, generator=gen, device="cuda")
+    d = hhr.make_dims(1, 3, G, P, n, n)
+    pt = torch.randperm(n, generator=gen, device="cuda").int().reshape(1, n)
+    q = torch.randn(1, 1, 3, D, generator=gen, device="cuda").bfloat16()
+    seq_len = torch.tensor([n * P], dtype=torch.int32, device="cuda")
+    blocks = torch.empty(1, 1, 1, m, dtype=torch.int32, device="cuda")
+    count = torch.empty(1, 1, 1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(hhr.hhr_block_select_workspace_bytes(d, 1), dtype=torch.uint8, device="cuda")
+    call = lambda: hhr.hhr_block_select(d, q, seq_len, None, pt, means, m, blocks, count, ws)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for length in (n * P, 7777, 0, 1):
+        q.copy_(torch.randn(1, 1, 3, D, generator=gen, device="cuda").bfloat16())
+        seq_len.fill_(length)
+        graph.replay()
+        status_ok()
+        ref = reference(q, means, pt, [length], None, P, 1, m)
+        assert torch.equal(count.cpu(), ref[1]) and torch.equal(blocks.cpu(), ref[0])
+
+
+def test_many_kv_heads():
+    """More KV heads than the single-token stream stages."""
+    build.build()
+    G, P, n = 70, 8, 200
+    gen = torch.Generator(device="cuda").manual_seed(10)
+    means = torch.randn(n, G, D, generator=gen, device="cuda")
+    d = hhr.make_dims(1, 2 * G, G, P, n, n)
+    pt = torch.randperm(n, generator=gen, device="cuda").int().reshape(1, n)
+    q = torch.randn(1, 1, 2 * G, D, generator=gen, device="cuda").bfloat16()
+    lens = [n * P - 3]
+    blocks, count = select(d, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), None, pt, means, 17)
+    status_ok()
+    ref = reference(q, means, pt, lens, None, P, G, 17)
+    assert torch.equal(count.cpu(), ref[1]) and torch.equal(blocks.cpu(), ref[0])
+
+
 def test_blocks_without_a_page_are_flagged_and_not_kept():
     build.build()
     c = Paged([320], 2, 2, 32, False, seed=5)

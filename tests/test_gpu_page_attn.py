@@ -88,6 +88,19 @@ def test_dense_long_sequence_peaked_and_flat(kv8):
 
 
 @pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("gs", [3, 7])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 4.0])
+def test_dense_scales(scale, gs, kv8):
+    """A scale of 0 (the plain mean), a negative and a large one (one key takes nearly all)."""
+    build.build()
+    c = Paged([700, 1, 0], 2, gs, 32, kv8, seed=13)
+    q = c.queries(3)
+    out, lse = dense(c, q, scale=scale)
+    status_ok()
+    check_dense(c, q, out, lse, scale)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
 def test_dense_large_and_small_magnitudes(kv8):
     """Queries and keys far from 1, with one key or value row at another exponent than the rest."""
     build.build()
@@ -340,6 +353,63 @@ def test_nan_and_infinite_keys_act_on_their_heads_only(kv8):
     clean = torch.arange(D, device="cuda") != 9
     assert torch.isfinite(out[0, 2:][:, clean]).all() and torch.isfinite(out[1]).all()
     assert torch.isfinite(lse[0, 2:]).all() and torch.isfinite(lse[1]).all()
+
+
+def test_infinite_keys_of_a_bf16_cache():
+    """A key that is +-infinite in a channel: heads whose logit is -inf leave it out, heads whose
+    logit is +inf (or NaN) become NaN, as the formula says."""
+    build.build()
+    c = Paged([300], 1, 4, 32, False, seed=82)
+    phys = int(c.pt[0, 5])
+    c.k[phys, 0, 9, 4] = math.inf                       # position 169
+    q = c.queries(1)
+    q[0, :, 4] = torch.tensor([-1.0, 2.0, -0.5, 0.0]).bfloat16().cuda()
+    out, lse = dense(c, q)
+    status_ok()
+    pos = torch.arange(300, device="cuda")
+    pos = pos[pos != 169]
+    k, v = c.rows("k", 0, 0, pos), c.rows("v", 0, 0, pos)
+    for h in (0, 2):
+        check_rows(out[0, h:h + 1], lse[0, h:h + 1], q[0, h:h + 1], k, v, SCALE, f"head {h}")
+    assert torch.isnan(out[0, 1]).all() and torch.isnan(out[0, 3]).all()
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Calls that overlap, each with its own workspace, do not disturb one another."""
+    build.build()
+    a, b = Paged([20000], 2, 4, 32, False, seed=84), Paged([15000, 300], 2, 4, 16, True, seed=85)
+    qa, qb = a.queries(1), b.queries(2)
+    ra, rb = dense(a, qa)[0].clone(), dense(b, qb)[0].clone()
+    torch.cuda.synchronize()
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(20):
+        with torch.cuda.stream(s):
+            got.append((dense(a, qa)[0], ra))
+        with torch.cuda.stream(t):
+            got.append((dense(b, qb)[0], rb))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in got)
+    status_ok()
+
+
+def test_a_call_sees_what_the_kernels_before_it_wrote():
+    """Every call's first kernel is placed while the one before it still runs: its inputs (written
+    just before, by other kernels of the stream) must nevertheless be the new ones."""
+    build.build()
+    c = Paged([3000, 500], 2, 4, 32, True, seed=86)
+    big = torch.randn(1 << 24, device="cuda")
+    q, outs, qs = c.queries(2), [], []
+    ws = torch.empty(hhr.hhr_paged_attn_workspace_bytes(c.d), dtype=torch.uint8, device="cuda")
+    for i in range(8):
+        new = c.queries(2)
+        big.mul_(1.0001)                                # keeps the GPU busy
+        q.copy_(new)
+        outs.append(dense(c, q, ws=ws))
+        qs.append(new)
+    status_ok()
+    for new, (out, lse) in zip(qs, outs):
+        check_dense(c, new, out, lse)
 
 
 def test_cache_rows_past_2_to_31_bytes():

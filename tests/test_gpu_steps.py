@@ -1,0 +1,156 @@
+"""The caches and steps together, as a decode loop uses them: a prompt written, then tokens appended
+and attended to, dense and block-sparse, in bf16 and 8 bits, beside the hash path on the same cache."""
+import math
+
+import pytest
+import torch
+
+import hhr_synth as S
+from hash_hierarchical_top_b200 import BlockStep, DecodeStep, DenseStep, KV8Cache, LayerCache, build, hhr
+from page_helpers import D, check_rows, status_ok, values_of
+from parity_helpers import dims_of
+
+pytestmark = pytest.mark.gpu
+SCALE = 1.0 / math.sqrt(D)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def rows_of(cache, pt, b, g, pos, P):
+    """float64 rows of a KV8Cache: K and V of sequence b, KV head g at pos."""
+    phys, slot = pt[b, pos // P].long(), pos % P
+    return [values_of(x.view(torch.uint8)[phys, g, slot], e[phys, g, slot])
+            for x, e in ((cache.k, cache.k_exp), (cache.v, cache.v_exp))]
+
+
+def test_decode_loop_over_an_8bit_cache():
+    """Two layers of one small model: layer 0 dense, layer 1 block-sparse. Every token is written
+    (layer 0 by the attention call, layer 1 by the append) and attended to; the dense step is
+    captured once and replayed, as a serving loop does."""
+    build.build()
+    B, G, gs, P, maxp, m = 2, 2, 4, 16, 20, 5
+    lens = [100, 33]
+    d = hhr.make_dims(B, G * gs, G, P, maxp, B * maxp)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    bf = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()
+    pt = torch.randperm(B * maxp, generator=gen, device="cuda").int().reshape(B, maxp)
+    caches = [KV8Cache(d, "cuda"), KV8Cache(d, "cuda", block_means=True)]
+    dense = DenseStep(d, "cuda", torch.bfloat16)
+    block = BlockStep(d, 1, m, "cuda", sink_pages=1, local_pages=1)
+    prompt = [bf(B, max(lens), 2 * G, D) for _ in caches]
+    for c, x in zip(caches, prompt):
+        c.append(x[:, :, :G], x[:, :, G:], i32([0, 0]), i32(lens), pt)
+    q, kn, vn = bf(B, G * gs, D), bf(B, G, D), bf(B, G, D)
+    seq_len, one = i32(lens), i32([1, 1])
+    seq_len += 1
+    dense.attend(q, caches[0], pt, seq_len, kn, vn)          # outside a capture first
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dense.attend(q, caches[0], pt, seq_len, kn, vn)
+    for step in range(20):
+        n = [x + 1 + step for x in lens]
+        seq_len.copy_(i32(n))
+        q.copy_(bf(B, G * gs, D)); kn.copy_(bf(B, G, D)); vn.copy_(bf(B, G, D))
+        graph.replay()
+        caches[1].append(kn, vn, seq_len - 1, one, pt)
+        out = block.step(q[:, None], caches[1], pt, seq_len)
+        status_ok()
+        for b in range(B):
+            for g in range(G):
+                h = slice(g * gs, (g + 1) * gs)
+                pos = torch.arange(n[b], device="cuda")
+                k, v = rows_of(caches[0], pt, b, g, pos, P)
+                check_rows(dense.out[b, h], dense.lse[b, h], q[b, h], k, v, SCALE, f"dense {step}")
+                mine = block.blocks[b, 0, g, :int(block.count[b, 0, g])].tolist()
+                pages = -(-n[b] // P)
+                assert len(mine) == min(m, pages) and 0 in mine and pages - 1 in mine
+                k, v = rows_of(caches[1], pt, b, g, pos, P)
+                means = torch.stack([k[p * P:(p + 1) * P].mean(0) for p in range(pages)])
+                s = means @ q[b, h].double().sum(0)
+                left = [p for p in range(pages) if p not in mine]
+                if left:   # fp32 means: scores may differ by their rounding
+                    free = [p for p in mine if p not in (0, pages - 1)]
+                    assert s[free].min() >= s[left].max() - 1e-4
+                at = torch.cat([torch.arange(p * P, min(n[b], (p + 1) * P)) for p in mine]).cuda()
+                check_rows(out[b, 0, h], block.lse[b, 0, h], q[b, h], k[at], v[at], SCALE, f"block {step}")
+    k_out, v_out = (torch.zeros(B, max(lens) + 20, G, D, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    caches[0].read(i32([0, 0]), seq_len, pt, k_out, v_out)
+    status_ok()
+    for b in range(B):
+        for g in range(G):
+            k, v = rows_of(caches[0], pt, b, g, torch.arange(int(seq_len[b]), device="cuda"), P)
+            assert torch.equal(k_out[b, :len(k), g].double(), k)
+            assert torch.equal(v_out[b, :len(v), g].double(), v)
+
+
+def test_steps_beside_the_hash_path_on_one_bf16_cache():
+    """The hash step, dense attention and block attention on the same cache and page table: the
+    dense step is the hash step with every key selected; block attention takes the pages that the
+    hash path's bounds kept (its trace) and those of the block means that the encoder writes."""
+    build.build()
+    wl = S.scaled(S.WORKLOADS["llama8b_32k"], batch=2, seq_lens=(3000, 1700), top_k=3200, m_pages=12,
+                  keep_div=0)
+    inp = S.make_inputs(wl, device="cuda")
+    d = dims_of(wl, inp)
+    P, G, gs = wl.page_size, wl.n_kv_heads, wl.n_q_heads // wl.n_kv_heads
+    cache = LayerCache(d, "cuda", block_means=True)
+    zero = i32([0, 0])
+    hashed = DecodeStep(d, hhr.HHR_MODE_HASH, wl.m_pages, 0, wl.top_k, "cuda")
+    # The per-page encoder writes the block means too.
+    hhr.hhr_encode_keys(d, inp["k_cache"], inp["page_table"], zero, inp["seq_len"], 3000, inp["R"],
+                        inp["W"], cache.page_minmax, cache.codes, cache.block_mean)
+    kept = torch.empty(2, G, hashed.m_max, dtype=torch.int32, device="cuda")
+    kept_count = torch.empty(2, G, dtype=torch.int32, device="cuda")
+    hashed.select(inp["q"], inp["seq_len"], inp["page_table"], cache, R=inp["R"], W=inp["W"],
+                  trace=hhr.make_trace(kept=kept, kept_count=kept_count))
+    pair = (inp["k_cache"], inp["v_cache"])
+
+    def logical(x, b, g, pos):
+        return x[inp["page_table"][b, pos // P].long(), g, pos % P].double()
+
+    def check(out, lse, blocks, count, what):
+        for b, n in enumerate(wl.seq_lens):
+            for g in range(G):
+                pos = (blocks[b, g, :int(count[b, g])].long()[:, None] * P +
+                       torch.arange(P, device="cuda")).reshape(-1)
+                pos = pos[pos < n]
+                h = slice(g * gs, (g + 1) * gs)
+                check_rows(out[b, h], lse[b, h], inp["q"][b, h], logical(pair[0], b, g, pos),
+                           logical(pair[1], b, g, pos), SCALE, what)
+
+    block = BlockStep(d, 1, wl.m_pages, "cuda")
+    block.blocks.copy_(kept[:, None])
+    block.count.copy_(kept_count[:, None])
+    block.attend(inp["q"][:, None], pair, inp["page_table"], inp["seq_len"])
+    status_ok()
+    check(block.out[:, 0], block.lse[:, 0], kept, kept_count, "kept pages")
+    block.step(inp["q"][:, None], pair, inp["page_table"], inp["seq_len"], cache.block_mean)
+    status_ok()
+    assert (block.count == wl.m_pages).all()
+    check(block.out[:, 0], block.lse[:, 0], block.blocks[:, 0], block.count[:, 0], "mean blocks")
+    dense = DenseStep(d, "cuda")
+    dense.attend(inp["q"], pair, inp["page_table"], inp["seq_len"])
+    pages = inp["page_table"].shape[1]
+    every = torch.arange(pages, dtype=torch.int32, device="cuda").expand(2, G, pages)
+    check(dense.out, dense.lse, every, torch.full((2, G), pages), "dense")
+    idx = torch.arange(3200, dtype=torch.int32, device="cuda").expand(2, G, 3200).contiguous()
+    hashed.idx.copy_(idx)
+    hashed.count.copy_(inp["seq_len"].view(2, 1).expand(2, G))
+    hashed.attend(inp["q"], *pair, inp["page_table"], inp["seq_len"])
+    status_ok()
+    # Both within 2e-3 of the formula relative to the row's largest channel (the token-list
+    # attention's stated tolerance), so within twice that of one another.
+    top = dense.out.abs().amax(-1, keepdim=True)
+    assert ((dense.out - hashed.out).abs() <= 4e-3 * top).all()
+
+
+def test_unsupported_sizes_are_refused():
+    d = hhr.make_dims(1, 8, 2, 16, 4, 4, head_dim=64)
+    for make in (lambda: DenseStep(d, "cuda"), lambda: BlockStep(d, 1, 2, "cuda"),
+                 lambda: BlockStep(hhr.make_dims(1, 8, 2, 16, 4, 4), 0, 2, "cuda"),
+                 lambda: BlockStep(hhr.make_dims(1, 8, 2, 16, 4, 4), 1, 0, "cuda")):
+        with pytest.raises(ValueError):
+            make()
