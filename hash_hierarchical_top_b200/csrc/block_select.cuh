@@ -9,8 +9,13 @@
 // within E of the m-th largest s (tau), so a block with s > tau + 2E is kept and one with
 // s < tau - 2E is not. The blocks in between (nearly always the cut itself, alone) are scored
 // again in 64 bits, where bf16 x fp32 products are exact and 128 of them sum to 2^-45 of their
-// size. Scoring everything in 64 bits instead took 29 us where the fp32 stream takes 23 us (8
-// sequences of 4096 blocks x 8 groups: 134 MB), bound by conversions and 64-bit latencies.
+// size. Scoring everything in 64 bits took 22.7 us where the fp32 tiles take 11.4 (64 queries x 8
+// groups over 1024 blocks, cold caches); the single-token stream takes 28 us either way.
+//
+// Measured (calls in a row): 8 sequences of 4096 blocks x 8 groups, one token each, 37 us: a stream
+// of 134 MB (20.5 us at the copy rate; 27.5 us with its launch and the three dependent loads that
+// precede the first means) and a choice that is a chain of barriers on 64 CTAs (about 6 us); 64
+// queries over 1024 blocks 19.8 us, all latency.
 //
 // E = kBsErr ||A|| max_p ||mean_p||, A_c = sum_h |q_hc|: the fp32 sum over at most 8 heads is off
 // by 7 units of 2^-24 of A_c, products and sums over 128 channels by at most 16 + 8 (chains of
@@ -120,17 +125,13 @@ __device__ __forceinline__ int bs_blocks(const BlockSelectArgs& a, int b) {
 }
 
 // One row per KV group (single tokens): a stream over the means. The means of a page's KV groups
-// lie side by side (512 G bytes), so the rows of a sequence are taken in the order (page, group):
-// with one (group, 512-byte piece of many pages) per warp instead, DRAM gave 4.6 TB/s of the
-// measured 6.5. The pages of all sequences are laid end to end and divided evenly over a grid
+// lie side by side (512 G bytes), so the rows of a sequence are taken in the order (page, group),
+// as they lie in memory. The pages of all sequences are laid end to end and divided evenly over a grid
 // that fills the GPU; warp w of a CTA takes the rows 16 w .. 16 w + 15, then those 64 on. 8 lanes
 // share a row, in registers: as soon as a row has been multiplied, its registers take the row of
 // the same place in the warp's next item (8 KB in flight per warp).
 constexpr int kBvWarps = 4;
-#ifndef HHR_BV_CTAS
-#define HHR_BV_CTAS 3
-#endif
-constexpr int kBvCtasPerSm = HHR_BV_CTAS;
+constexpr int kBvCtasPerSm = 3;  // 4 spill, and are no faster
 constexpr int kBvItem = 16;      // rows of an item
 constexpr int kBvMaxGroups = 64; // KV groups whose query sums are staged
 inline size_t block_stream_smem(int G) { return (size_t)G * kD * 4; }

@@ -1032,23 +1032,22 @@ int launch_first(int prof, void (*kernel)(Args), dim3 grid, int threads, size_t 
 }
 
 // CTAs of the cluster that takes one row, or 0 for even shares of all rows' keys with a join.
-// Clusters need one launch and no join, but split every row alike: they are taken where all rows'
-// clusters are resident at once, for lists (rows of one capacity), and for dense rows of up to
-// HHR_PA_DENSE_CLUSTER keys (or of a single sequence up to HHR_PA_DENSE_CLUSTER1).
-#ifndef HHR_PA_DENSE_CLUSTER
-#define HHR_PA_DENSE_CLUSTER 2048
-#endif
-#ifndef HHR_PA_DENSE_CLUSTER1
-#define HHR_PA_DENSE_CLUSTER1 4096
-#endif
-#ifndef HHR_PA_LIST_CLUSTER
-#define HHR_PA_LIST_CLUSTER 1
-#endif
+// Clusters need one launch and no join, but split every row alike and use at most 8 CTAs per row.
+// They are taken where all rows' clusters are resident at once, and
+//   - dense rows can hold at most 2048 keys (lengths may differ: a longer row would leave the
+//     other clusters waiting), or 4096 for a single sequence (rows of one length). Measured, 8 KV
+//     heads, bf16: 8 sequences of 2K keys 16.3 us against 20.2 us with even shares; 1 sequence of
+//     4K keys 10.5 against 10.8 us, of 8K keys 16.0 against 14.6 us;
+//   - lists hold at most 4096 keys, or there are rows enough for half of the GPU's CTAs (8
+//     sequences x 64 pages: 12.8 us against 15.3 us; 1 sequence x 256 pages: 13.2 against 12.3 us).
+constexpr long long kDenseClusterKeys = 2048, kOneClusterKeys = 4096;
 int page_cluster(const hhr_dims* d, int T, int blocks, bool list) {
   const long long rows = (long long)d->batch * T * sel_rows(d);
   const long long keys = (long long)blocks * d->page_size, n = (long long)kPcCtasPerSm * sm_count();
-  if (rows > n || (list && !HHR_PA_LIST_CLUSTER)) return 0;
-  if (!list && keys > (d->batch == 1 ? HHR_PA_DENSE_CLUSTER1 : HHR_PA_DENSE_CLUSTER)) return 0;
+  if (rows > n) return 0;
+  if (list ? keys > kOneClusterKeys && 2 * rows * kPaMaxCluster < n
+           : keys > (d->batch == 1 ? kOneClusterKeys : kDenseClusterKeys))
+    return 0;
   // As many as fit at once, and no more than the row has units.
   return (int)max(1LL, min((long long)kPaMaxCluster, min(n / rows, (keys + kUnitKeys - 1) / kUnitKeys)));
 }

@@ -9,21 +9,26 @@
 // of a row by page_join_kernel.
 //
 // What bounds it: the K/V bytes (512 B per key and KV head in bf16, 258 B in 8 bits) against 4
-// flops per byte and head, far below the tensor cores' balance. So the design keeps loads in
+// flops per byte and head, far below the tensor cores' balance. So the design keeps copies in
 // flight and spends few instructions per byte:
-//   - K and V go from global memory straight into registers as 16-byte loads in the layout that
-//     the matrix instructions want, with no pass through shared memory and no barrier in the
-//     loop: 16 warps of 8 KB each keep 128 KB in flight per SM. The order of the channels in a
-//     dot product is free, so lane (g, t) = (lane / 4, lane % 4) of S = Q K^T loads whole 16-byte
-//     pieces t, t + 4, ... of key g and the query fragments follow that order; in O^T = V^T P^T
-//     the channels are the rows of A, so a lane that holds 16-byte pieces of the keys 2t, 2t + 1,
-//     2t + 8, 2t + 9 only interleaves key pairs (one byte permute per register).
-//   - S^T = K Q^T has the keys on M = 16 and the heads on N = 8; its weights become the B operand
-//     of O^T = V^T P^T (channels on M, heads on N) by one 8 x 8 transposition per 8 keys.
-//   - Page ids are loaded two steps ahead of the rows they locate, the rows one step ahead of
-//     their use.
+//   - every warp runs on its own: it copies its next 16 (8-bit: 32) keys' K and V rows (8 KB) into
+//     its own ring in shared memory with cp.async while it computes on the present ones; no
+//     barrier in the loop, 12 warps and 96 KB in flight per SM. Loading the operands straight into
+//     registers (16 warps, 128 KB) reached 5.1 TB/s where this reaches 6.8 (8 x 128K keys): it
+//     spent more instructions, and its 64-byte requests split DRAM bursts.
+//   - S^T = K Q^T has the keys on M = 16 and the heads on N = 8 (S = Q K^T would leave half of M
+//     empty); its weights become the B operand of O^T = V^T P^T (channels on M, heads on N) by
+//     one 8 x 8 transposition per 8 keys. With up to 4 heads the two parts of a weight fill the 8
+//     columns of one product. Together that is half the matrix instructions of the plain layout:
+//     under the 1000 W power cap the ragged 8-bit batch went from 447 to 403 us by this alone.
+//   - a page id is loaded a step before the row index that needs it, and nothing loaded is looked
+//     at in the step that loads it.
 // P is used in parts (bf16: three, f16: two), so that the fp32 output is not limited by the matrix
-// operands' type.
+// operands' type: 2e-7 to 5e-7 off the 64-bit result at 517 to 128K keys.
+//
+// Measured (B200, calls in a row): 8 x 128K keys x 8 KV heads in bf16 620-630 us, 6.8-6.9 TB/s of K
+// and V (the measured copy rate is 6.55); 16 ragged sequences of 8K to 128K keys in 8 bits 388-408
+// us, 6.2-6.5 TB/s; 1 x 32K keys 30.3 us, of which the stream takes 21; 1 x 517 keys 5.9 us.
 //
 // 8-bit cache: e4m3 numbers become f16 exactly. Q is scaled by a power of two per head so that
 // its largest channel is in [2^14, 2^15): bf16 queries are then exact in f16 down to 2^-38 of
@@ -32,9 +37,10 @@
 // 2^14 more keeps small weights out of f16's subnormal range.
 //
 // Split of the work: the rows' keys, in units of kUnitKeys, are laid end to end and divided
-// evenly over the CTAs (two per SM), whatever the lengths; a CTA's share covers the end of one
+// evenly over the CTAs (three per SM), whatever the lengths; a CTA's share covers the end of one
 // row, whole rows, the beginning of another. Whole rows are written directly; a share that
-// covers part of a row writes a partial (at most two per CTA), joined by page_join_kernel.
+// covers part of a row writes a partial (at most two per CTA), joined by page_join_kernel. Short
+// rows are split over a cluster instead (page_cluster_kernel).
 #pragma once
 #include "attn.cuh"
 #include "common.cuh"

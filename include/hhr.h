@@ -339,7 +339,9 @@ int hhr_read_kv8(const hhr_dims* dims, const uint8_t* k, const uint8_t* v, const
  *              the call runs on. Its contents need not be kept or cleared, but calls that can
  *              overlap on the GPU need one each.
  * The keys of all rows are divided evenly over the GPU, whatever the sequences' lengths; rows
- * that are split are joined in a fixed order, so that equal inputs give equal bits. */
+ * that are split are joined in a fixed order, so that equal inputs give equal bits. The first
+ * call of a kind on a device loads its kernel and raises its shared-memory limit: make it before
+ * capturing the call into a CUDA graph (this holds for hhr_block_select too). */
 
 size_t hhr_paged_attn_workspace_bytes(const hhr_dims* dims);
 
