@@ -1101,7 +1101,7 @@ int check_page_attn(const hhr_dims* d, const uint16_t* q, const void* k, const v
       seq_len == nullptr || out == nullptr)
     return HHR_ERR_INVALID_ARG;
   if ((k_exp == nullptr) != (v_exp == nullptr)) return HHR_ERR_INVALID_ARG;
-  if (!(scale == scale) || isinf(scale)) return HHR_ERR_INVALID_ARG;
+  if (!isfinite(scale * 1.4426950408889634f)) return HHR_ERR_INVALID_ARG;
   if (out_bf16 != 0 && out_bf16 != 1) return HHR_ERR_INVALID_ARG;
   if (misaligned16({q, k, v, k_exp, v_exp, out, lse})) return HHR_ERR_INVALID_ARG;
   return rows_fit(d) ? HHR_OK : HHR_ERR_UNSUPPORTED;

@@ -200,27 +200,27 @@ struct RowKeys {
 // Locating a key takes three steps, each of which uses what the one before it loaded. The loop
 // runs them one iteration apart and leaves a loaded value alone until the next iteration (a use
 // at once would stall the warp for the load's latency in every step).
-constexpr int kNoKey = (int)0x80000000;  // a slot that holds no key
-// The block of slot j: dense, its page; list, the entry as it is listed.
+// The block of slot j: dense, its page; list, the entry as it is listed (j >= k1: none).
 template <bool kList>
 __device__ __forceinline__ int load_block(const PageAttnArgs& a, const RowKeys& r, int j, int k1) {
-  if (j >= k1) return kNoKey;
+  if (j >= k1) return -1;
   return kList ? r.blocks[page_of(a, j)] : page_of(a, j);
 }
-// The page-table entry of a loaded block, and kNoKey where it is not a block with keys.
+// The page-table entry of a loaded block; the block becomes -1 where slot j holds no key.
 template <bool kList>
-__device__ __forceinline__ int load_page(const PageAttnArgs& a, const RowKeys& r, int& block) {
-  if (kList && block != kNoKey && (block < 0 || block >= a.maxp)) {
+__device__ __forceinline__ int load_page(const PageAttnArgs& a, const RowKeys& r, int& block, int j,
+                                         int k1) {
+  if (kList && j < k1 && (block < 0 || block >= a.maxp)) {
     flag_status(kStatusBadToken);
-    block = kNoKey;
+    block = -1;
   }
-  if (block == kNoKey || block * a.P >= r.limit) return kNoKey;
-  return r.pages[block];
+  if (block >= 0 && block * a.P >= r.limit) block = -1;
+  return block >= 0 ? r.pages[block] : 0;
 }
 // The cache row of slot j, or kNoRow.
 __device__ __forceinline__ uint32_t row_of(const PageAttnArgs& a, const RowKeys& r, int j,
                                            int block, int page) {
-  if (page == kNoKey) return kNoRow;
+  if (block < 0) return kNoRow;
   if (page < 0 || page >= a.n_phys) {
     flag_status(kStatusBadPage);
     return kNoRow;
@@ -300,7 +300,7 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
 #pragma unroll
     for (int i = 0; i <= NS; ++i) bl[i] = load_block<kList>(a, rk, j0 + i * stride, k1);
 #pragma unroll
-    for (int i = 0; i < NS; ++i) pg[i] = load_page<kList>(a, rk, bl[i]);
+    for (int i = 0; i < NS; ++i) pg[i] = load_page<kList>(a, rk, bl[i], j0 + i * stride, k1);
 #pragma unroll
     for (int i = 0; i < NS - 1; ++i) {
       rq[i] = row_of(a, rk, j0 + i * stride, bl[i], pg[i]);
@@ -366,7 +366,7 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
     issue(rq[NS - 1], st == 0 ? NS - 1 : st - 1);
     cp_async_commit();
     blk1 = blk2;
-    page1 = load_page<kList>(a, rk, blk1);
+    page1 = load_page<kList>(a, rk, blk1, j0 + stride, k1);
     blk2 = load_block<kList>(a, rk, j0 + 2 * stride, k1);
     const uint32_t ks = ring + (uint32_t)st * kPaStage, vs = ks + kPaTile;
     // 8-bit: the exponent bytes of the row that this lane located (K, V); 0 for none.
@@ -476,7 +476,7 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
       }
     // O^T = corr O^T + V^T P^T. The step's products are summed from zero and added in fp32: the
     // matrix units truncate when they add to an accumulator, and over thousands of steps that
-    // is a bias (8e-6 of the output at 128K keys; 1e-6 this way).
+    // is a bias (8e-6 of the output at 128K keys; 5e-7 this way).
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -594,13 +594,13 @@ __device__ __forceinline__ RowKeys row_keys(const PageAttnArgs& a, int row, int 
 }
 
 // Dense: writes the newest row (position rk.n - 1) of sequence b into the cache; by the CTA that
-// reads it, before the barrier behind which it does.
+// reads it, before the barrier behind which it does. A length past the page table has no such row.
 template <bool K8>
 __device__ __forceinline__ void append_row(const PageAttnArgs& a, const RowKeys& rk, int b) {
   const int tid = threadIdx.x, t = rk.n - 1, l16 = tid & 15;
-  if (tid >= 32) return;
+  if (tid >= 32 || a.seq_len[b] > a.maxp * a.P) return;
   int lp = page_of(a, t);
-  const int page = load_page<false>(a, rk, lp);
+  const int page = load_page<false>(a, rk, lp, t, rk.n);
   const uint32_t o = row_of(a, rk, t, lp, page);
   if (o == kNoRow) return;
   const uint16_t* src = (tid < 16 ? a.k_new : a.v_new) + ((size_t)b * a.G + rk.g) * kD;

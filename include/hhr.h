@@ -331,7 +331,8 @@ int hhr_read_kv8(const hhr_dims* dims, const uint8_t* k, const uint8_t* v, const
  * Two calls that attend to every key of the pages they are given, from a bf16 cache (k_exp and
  * v_exp NULL) or an 8-bit one. out[..][h] = sum_j softmax_j(scale * q_h . k_j) v_j, with
  * statistics and sums in fp32; a row with no key gives zeros. Keys outside the mask are never
- * read into the sums, whatever the cache holds there.
+ * read into the sums, whatever the cache holds there; keys whose logit is -inf have weight 0; a
+ * NaN key or a logit of +inf makes its head's output NaN, an infinite or NaN value its channel.
  *   out      : [B][T][Hq][d], f32, or bf16 with out_bf16 = 1 (rounded once)
  *   lse      : NULL, or f32 [B][T][Hq]: log sum_j exp(scale * q_h . k_j), with which outputs
  *              over disjoint key sets can be joined; -inf for a row with no key
@@ -352,7 +353,7 @@ size_t hhr_paged_attn_workspace_bytes(const hhr_dims* dims);
  *                  the cache (quantised as hhr_append_kv8 does, when it holds 8 bits) by this
  *                  call before they are attended to. A sequence of length 0 writes nothing.
  *   dims.select_per_head must be 0. seq_len[b] beyond max_pages_per_seq * P is clipped to it
- *   and flagged; a key whose page-table entry is out of range is skipped and flagged. */
+ *   and flagged (its new row, which has no page, is not written); a key whose page-table entry is out of range is skipped and flagged. */
 int hhr_paged_attn(const hhr_dims* dims, const uint16_t* q, const uint16_t* k_new,
                    const uint16_t* v_new, void* k_cache, void* v_cache, uint8_t* k_exp,
                    uint8_t* v_exp, const int32_t* page_table, const int32_t* seq_len, float scale,

@@ -133,7 +133,7 @@ def test_paged_attention_arguments(L):
     assert paged(L, d, ke=P) == INV and paged(L, d, ve=P) == INV
     assert paged(L, d, ke=BAD, ve=P) == INV
     assert paged(L, d, bf16=2) == INV
-    for x in ("nan", "inf", "-inf"):
+    for x in ("nan", "inf", "-inf", "3e38"):   # (also times log2 e)
         assert paged(L, d, scale=ctypes.c_float(float(x))) == INV
     assert paged(L, _d(select_per_head=1)) == INV       # nothing is selected
     assert paged(L, _d(n_q_heads=72)) == UNS            # 9 heads per KV head

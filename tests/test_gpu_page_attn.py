@@ -355,6 +355,44 @@ def test_nan_and_infinite_keys_act_on_their_heads_only(kv8):
     assert torch.isfinite(lse[0, 2:]).all() and torch.isfinite(lse[1]).all()
 
 
+@pytest.mark.parametrize("pages", [3, 400])
+@pytest.mark.parametrize("kv8", [False, True])
+def test_a_new_row_without_a_page_is_not_written(kv8, pages):
+    """A length past the page table, or a newest page that is out of range: flagged, and no row of
+    the cache is touched (by a cluster's kernel and by the even shares')."""
+    build.build()
+    n = pages * 16
+    c = Paged([n, n], 1, 2, 16, kv8, seed=83, extra_cols=0)
+    assert c.maxp * 16 == n
+    new = torch.randn(2, 1, D, device="cuda").bfloat16()
+    before = [x.clone() for x in (c.k, c.v, c.k_exp, c.v_exp) if x is not None]
+    q = c.queries(2)
+    for page, bits in ((c.n_phys, 1), (-1, 1), (-(1 << 31), 1)):
+        good = int(c.pt[0, -1])
+        c.pt[0, -1] = page
+        c.seq_len[1] = n + 1                               # sequence 1 has no page for it
+        dense(c, q, k_new=new, v_new=new)
+        torch.cuda.synchronize()
+        assert hhr.hhr_read_device_status() == (hhr.HHR_ERR_DEVICE_STATUS, bits | 2)
+        c.pt[0, -1] = good
+        for x, y in zip([x for x in (c.k, c.v, c.k_exp, c.v_exp) if x is not None], before):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_extreme_list_entries_are_flagged():
+    build.build()
+    c = Paged([200], 1, 2, 32, False, seed=87)
+    q = c.queries(1)
+    for entry in (-(1 << 31), (1 << 31) - 1, -1):
+        blocks = torch.tensor([[[[entry, 2, 5]]]], dtype=torch.int32, device="cuda")
+        count = torch.full((1, 1, 1), 9, dtype=torch.int32, device="cuda")   # clipped to 3
+        out, lse = sparse(c, q[:, None], blocks, count, None)
+        torch.cuda.synchronize()
+        assert hhr.hhr_read_device_status() == (hhr.HHR_ERR_DEVICE_STATUS, 2)
+        pos = torch.cat([torch.arange(64, 96), torch.arange(160, 192)]).cuda()
+        check_rows(out[0, 0], lse[0, 0], q[0], c.rows("k", 0, 0, pos), c.rows("v", 0, 0, pos), SCALE, "rest")
+
+
 def test_infinite_keys_of_a_bf16_cache():
     """A key that is +-infinite in a channel: heads whose logit is -inf leave it out, heads whose
     logit is +inf (or NaN) become NaN, as the formula says."""
