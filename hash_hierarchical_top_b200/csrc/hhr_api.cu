@@ -1252,11 +1252,12 @@ int hhr_block_select(const hhr_dims* d, int n_queries, const uint16_t* q, const 
   const long long stream_ctas = min(((long long)B * maxp * d->n_kv_heads + kBvItem - 1) / kBvItem,
                                     (long long)kBvCtasPerSm * sm_count());
   a.g_mul = page_mul(a.G);
-  // The choice: 128 threads per row of up to 1024 blocks (bound by barriers, and more rows fit an
-  // SM: 64 queries x 8 groups over 1024 blocks take 24.6 us in all against 30.9 us with 512), 512
-  // for longer rows (4096 blocks: 39 us in all against 49 us with 128).
-  const int wide = maxp > 1024;
-  void (*topm)(BlockSelectArgs) = wide ? block_topm_kernel<512> : block_topm_kernel<128>;
+  // The choice: 256 threads per row of up to 2048 blocks (its passes wait at barriers, and more
+  // rows fit an SM), 512 for longer rows. 64 queries x 8 groups, both kernels: 1024 blocks 17.8 us
+  // with 256 threads, 19.9 with 128; 2048 blocks 25.3 with 256, 33.0 with 512; 8 sequences of 4096
+  // blocks 37 us with 512, 41 with 256.
+  const int wide = maxp > 2048;
+  void (*topm)(BlockSelectArgs) = wide ? block_topm_kernel<512> : block_topm_kernel<256>;
   if (smem > kDefaultSmem && allow_smem(topm, smem, g_smem_topm[wide]) != cudaSuccess)
     return HHR_ERR_CUDA;
   if (single)
@@ -1270,7 +1271,7 @@ int hhr_block_select(const hhr_dims* d, int n_queries, const uint16_t* q, const 
   if (st != HHR_OK) return st;
   prof_begin(HHR_KERNEL_TOPM, s);
   const cudaError_t e = launch_pdl(topm, dim3((unsigned)(B * n_queries * Gs)),
-                                   dim3(wide ? 512 : 128), smem, s, a);
+                                   dim3(wide ? 512 : 256), smem, s, a);
   prof_end(HHR_KERNEL_TOPM, s);
   if (e != cudaSuccess) { g_last_cuda = e; return HHR_ERR_CUDA; }
   return HHR_OK;
