@@ -174,6 +174,30 @@ def test_long_rows_and_captured_calls():
         assert torch.equal(count.cpu(), ref[1]) and torch.equal(blocks.cpu(), ref[0])
 
 
+@pytest.mark.parametrize("T", [1, 2])
+def test_many_ragged_sequences(T):
+    """More sequences than a warp scans at once, empty ones among them."""
+    build.build()
+    P, G, m = 8, 2, 6
+    gen = torch.Generator(device="cuda").manual_seed(11)
+    lens = [(53 * i) % 700 if i % 7 else 0 for i in range(90)]
+    pages = [-(-n // P) for n in lens]
+    maxp, n_phys = max(pages), sum(pages)
+    pt = torch.full((90, maxp), -1, dtype=torch.int32, device="cuda")
+    order, at = torch.randperm(n_phys, generator=gen, device="cuda").int(), 0
+    for b, n in enumerate(pages):
+        pt[b, :n] = order[at:at + n]
+        at += n
+    means = torch.randn(n_phys, G, D, generator=gen, device="cuda")
+    d = hhr.make_dims(90, 6, G, P, maxp, n_phys)
+    q = torch.randn(90, T, 6, D, generator=gen, device="cuda").bfloat16()
+    seq_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    blocks, count = select(d, q, seq_len, None, pt, means, m)
+    status_ok()
+    ref = reference(q, means, pt, lens, None, P, G, m)
+    assert torch.equal(count.cpu(), ref[1]) and torch.equal(blocks.cpu(), ref[0])
+
+
 def test_many_kv_heads():
     """More KV heads than the single-token stream stages."""
     build.build()

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from hash_hierarchical_top_b200 import build, hhr
-from page_helpers import D, Paged, check_rows, quantise_ref, status_ok
+from page_helpers import D, Paged, check_rows, quantise_ref, status_ok, values_of
 
 pytestmark = pytest.mark.gpu
 SCALE = 1.0 / math.sqrt(D)
@@ -68,6 +68,26 @@ def test_dense_many_ragged_sequences(kv8):
     q = c.queries(300)
     out, lse = dense(c, q)
     status_ok()
+    check_dense(c, q, out, lse)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_dense_many_sequences_write_their_newest_rows(kv8):
+    build.build()
+    lens = [(29 * i) % 200 for i in range(100)]
+    c = Paged(lens, 2, 2, 16, kv8, seed=9)
+    new = [torch.randn(100, 2, D, device="cuda").bfloat16() for _ in "kv"]
+    q = c.queries(100)
+    out, lse = dense(c, q, k_new=new[0], v_new=new[1])
+    status_ok()
+    for b, n in enumerate(lens):
+        if n:
+            for name, x in zip("kv", new):
+                got = torch.stack([c.rows(name, b, g, torch.tensor([n - 1], device="cuda"))[0] for g in range(2)])
+                # The 8-bit row: half a step of 2^-4, or 2^(e - 10) below the smallest normal number.
+                x = x[b].double()
+                tol = (2.0 ** -4 * x.abs()).clamp(min=float(x.abs().max()) / 224 * 2.0 ** -10) if kv8 else 0
+                assert ((got - x).abs() <= tol).all()
     check_dense(c, q, out, lse)
 
 
@@ -448,6 +468,38 @@ def test_a_call_sees_what_the_kernels_before_it_wrote():
     status_ok()
     for new, (out, lse) in zip(qs, outs):
         check_dense(c, new, out, lse)
+
+
+def test_8bit_cache_past_4_gigabytes():
+    """Rows whose byte offsets pass 32 bits: appended, read back, attended to (dense and listed)."""
+    build.build()
+    P, G, n_phys, n = 256, 8, 16500, 700           # 16500 * 8 * 256 rows of 128 bytes: 4.3 GB
+    k, v = (torch.empty(n_phys, G, P, D, dtype=torch.uint8, device="cuda") for _ in "kv")
+    ke, ve = (torch.empty(n_phys, G, P, dtype=torch.uint8, device="cuda") for _ in "kv")
+    c = Paged([n], G, 4, P, True, seed=92)
+    for j in range(3):
+        c.pt[0, j] = n_phys - 1 - j
+    c.k, c.v, c.k_exp, c.v_exp, c.n_phys = k, v, ke, ve, n_phys
+    c.d.n_phys_pages = n_phys
+    new = [torch.randn(1, n, G, D, device="cuda").bfloat16() for _ in "kv"]
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    hhr.hhr_append_kv8(c.d, *new, zero, c.seq_len, c.pt, k, v, ke, ve)
+    back = [torch.empty(1, n, G, D, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    hhr.hhr_read_kv8(c.d, k, v, ke, ve, c.pt, zero, c.seq_len, *back)
+    q = c.queries(1)
+    out, lse = dense(c, q)
+    blocks = torch.tensor([2, 0, 1], dtype=torch.int32, device="cuda").expand(1, 1, G, 3).contiguous()
+    count = torch.full((1, 1, G), 3, dtype=torch.int32, device="cuda")
+    out2, lse2 = sparse(c, q[:, None], blocks, count, None)
+    status_ok()
+    pos = torch.arange(n, device="cuda")
+    for name, x, y in zip("kv", new, back):
+        rows = torch.stack([c.rows(name, 0, g, pos) for g in range(G)], 1)
+        assert torch.equal(y[0].double(), rows)
+        ref, exp = quantise_ref(x[0])
+        assert torch.equal(rows.cpu(), values_of(ref, exp))
+    check_dense(c, q, out, lse)
+    check_dense(c, q, out2[:, 0], lse2[:, 0])
 
 
 def test_cache_rows_past_2_to_31_bytes():
