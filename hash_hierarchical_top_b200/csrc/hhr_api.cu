@@ -1038,18 +1038,22 @@ int launch_first(int prof, void (*kernel)(Args), dim3 grid, int threads, size_t 
 //     other clusters waiting), or 4096 for a single sequence (rows of one length). Measured, 8 KV
 //     heads, bf16: 8 sequences of 2K keys 16.3 us against 20.2 us with even shares; 1 sequence of
 //     4K keys 10.5 against 10.8 us, of 8K keys 16.0 against 14.6 us;
-//   - lists hold at most 4096 keys, or there are rows enough for half of the GPU's CTAs (8
-//     sequences x 64 pages: 12.8 us against 15.3 us; 1 sequence x 256 pages: 13.2 against 12.3 us).
+//   - lists hold at most 4096 keys, or the clusters fill half of the GPU (up to 8192 keys) or three
+//     quarters of it. 8 sequences x 64 pages of 32: 12.8 us against 15.3 us; x 256 pages: 46.1
+//     against 49.5 us (bf16), 28.5 against 31.5 us (8-bit); but 4 sequences x 32K keys in 8 bits
+//     63.0 against 50.7 us, 1 sequence x 6K keys 15.2 against 12.2 us.
 constexpr long long kDenseClusterKeys = 2048, kOneClusterKeys = 4096;
 int page_cluster(const hhr_dims* d, int T, int blocks, bool list) {
   const long long rows = (long long)d->batch * T * sel_rows(d);
   const long long keys = (long long)blocks * d->page_size, n = (long long)kPcCtasPerSm * sm_count();
   if (rows > n) return 0;
-  if (list ? keys > kOneClusterKeys && 2 * rows * kPaMaxCluster < n
-           : keys > (d->batch == 1 ? kOneClusterKeys : kDenseClusterKeys))
-    return 0;
   // As many as fit at once, and no more than the row has units.
-  return (int)max(1LL, min((long long)kPaMaxCluster, min(n / rows, (keys + kUnitKeys - 1) / kUnitKeys)));
+  const long long cs =
+      max(1LL, min((long long)kPaMaxCluster, min(n / rows, (keys + kUnitKeys - 1) / kUnitKeys)));
+  const bool fit = !list ? keys <= (d->batch == 1 ? kOneClusterKeys : kDenseClusterKeys)
+                         : keys <= kOneClusterKeys || 4 * rows * cs >= 3 * n ||
+                               (keys <= 2 * kOneClusterKeys && 2 * rows * cs >= n);
+  return fit ? (int)cs : 0;
 }
 
 // Launches the page attention and, where CTAs can share a row, the join of its partials.
@@ -1153,6 +1157,7 @@ int hhr_append_kv8(const hhr_dims* d, const uint16_t* k_new, const uint16_t* v_n
   if (misaligned16({k_new, v_new, block_mean})) return HHR_ERR_INVALID_ARG;
   if (max_new == 0) return HHR_OK;
   const long long pages = (max_new + (long long)d->page_size - 1) / d->page_size + 1;
+  if (pages > 0x7fffffffLL) return HHR_ERR_UNSUPPORTED;
   AppendArgs a{k_new, v_new, start, n_new, page_table, k, v, k_exp, v_exp, block_mean,
                token_stride, d->n_kv_heads, d->page_size, d->max_pages_per_seq, d->n_phys_pages,
                max_new};

@@ -119,6 +119,7 @@ def test_append_and_read_arguments(L):
     assert append(L, d, max_new=0) == hhr.HHR_OK
     assert read(L, d, max_n=-1) == INV
     assert read(L, d, max_n=0) == hhr.HHR_OK
+    assert append(L, _d(page_size=1), max_new=(1 << 31) - 1) == UNS   # one page too many
     big = _d(page_size=256, n_phys_pages=1 << 21)       # 2^32 cache rows
     assert append(L, big) == UNS and read(L, big) == UNS
 
