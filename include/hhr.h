@@ -434,7 +434,8 @@ int hhr_profile_next(int kernel, void* start_event, void* stop_event);
 /* Synchronises `stream`, then returns HHR_OK if no device-side check fired since
  * the last call, else HHR_ERR_DEVICE_STATUS; clears the status word. If `bits` is
  * not NULL (host), receives the raw status bits (1 = bad page id, 2 = bad token
- * index, 4 = n_new clipped to max_new, 8 = a bounded wait in the tensor-core encoder
+ * index, block id, or length beyond the page table, 4 = n_new clipped to max_new
+ * (hhr_read_kv8: n to max_n), 8 = a bounded wait in the tensor-core encoder
  * gave up). */
 int hhr_read_device_status(void* stream, int* bits);
 
