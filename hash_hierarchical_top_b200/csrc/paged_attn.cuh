@@ -28,7 +28,7 @@
 //
 // Measured (B200, calls in a row): 8 x 128K keys x 8 KV heads in bf16 620-630 us, 6.8-6.9 TB/s of K
 // and V (the measured copy rate is 6.55); 16 ragged sequences of 8K to 128K keys in 8 bits 388-408
-// us, 6.2-6.5 TB/s; 1 x 32K keys 30.3 us, of which the stream takes 21; 1 x 517 keys 5.9 us.
+// us, 6.2-6.5 TB/s; 1 x 32K keys 30.3 us, of which the stream takes 21; 1 x 517 keys 5.7 us.
 //
 // 8-bit cache: e4m3 numbers become f16 exactly. Q is scaled by a power of two per head so that
 // its largest channel is in [2^14, 2^15): bf16 queries are then exact in f16 down to 2^-38 of
@@ -125,6 +125,12 @@ __device__ __forceinline__ UnitPlace dense_place(const PageAttnArgs& a, int* sh,
 // 16 bytes into shared memory.
 __device__ __forceinline__ void cp_async16_at(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+}
+// A word whose load is issued where it stands.
+__device__ __forceinline__ uint32_t ldg_u32_now(const uint32_t* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u32 %0, [%1];\n" : "=r"(v) : "l"(p));
+  return v;
 }
 __device__ __forceinline__ void prefetch_l1(const void* p) {
   asm volatile("prefetch.global.L1 [%0];\n" ::"l"(p) : "memory");
@@ -242,7 +248,10 @@ constexpr int kPaStage = 2 * kPaTile + 256;
 // Keys [k0, k1) of a row, over the CTA's warps: the state of every head is left in shared
 // memory (mo [warps][8][d], ml [warps][8][2], which reuse the rings). Ends with the state of
 // all warps written (a barrier).
-template <bool K8, bool kList, bool kPair, int NS>
+// kSoon issues the query loads before the first keys are located instead of after their copies:
+// a cluster's few steps gain the latency (517 keys 5.87 -> 5.72 us, lists of 64 blocks 12.85 ->
+// 12.63); the shares of bf16 rows lose 1% to the registers it holds, so that they load late.
+template <bool K8, bool kList, bool kPair, int NS, bool kSoon>
 __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKeys& rk,
                                              const uint16_t* q, int gs, int k0, int k1,
                                              char* smem, float* mo, float* ml) {
@@ -257,6 +266,20 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
   const uint32_t ring = smem_u32(smem) + (uint32_t)warp * (NS * kPaStage);
   const int base = k0 + warp * S, stride = kPaWarps * S;
   const int lk = K8 ? lane : (lane & 15);  // the key of a step that this lane locates
+
+  // The query words of column gq (see below).
+  const int head = kPair ? gq & 3 : gq;
+  const bool hv = head < gs;
+  uint32_t qa[8][2];
+  auto load_q = [&] {
+    const uint32_t* q2 = reinterpret_cast<const uint32_t*>(q + (size_t)(hv ? head : 0) * kD);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      qa[i][0] = ldg_u32_now(q2 + 8 * i + (K8 ? 2 * tq : tq));
+      qa[i][1] = ldg_u32_now(q2 + 8 * i + (K8 ? 2 * tq + 1 : tq + 4));
+    }
+  };
+  if constexpr (kSoon) load_q();
 
   // Copies the rows of a step (`row`: this lane's) into stage st; missing rows become zeros.
   const char* kl = kb + 16 * (lane % RC);
@@ -317,17 +340,14 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
   // 2tq + 9 are the channels 16i + 4tq + {0, 1, 2, 3}.
   // A negative scale goes into the queries' signs, so that the largest product is the largest
   // logit: logit = hs * product in log2 units, hs > 0 (a scale of 0 becomes the smallest number).
-  uint32_t qa[8][2];
+  if constexpr (!kSoon) load_q();
   float hs = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
   {
-    const int head = kPair ? gq & 3 : gq;
-    const bool hv = head < gs;
     const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-    const uint32_t* q2 = reinterpret_cast<const uint32_t*>(q + (size_t)(hv ? head : 0) * kD);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      qa[i][0] = hv ? q2[8 * i + (K8 ? 2 * tq : tq)] ^ sign : 0u;
-      qa[i][1] = hv ? q2[8 * i + (K8 ? 2 * tq + 1 : tq + 4)] ^ sign : 0u;
+      qa[i][0] = hv ? qa[i][0] ^ sign : 0u;
+      qa[i][1] = hv ? qa[i][1] ^ sign : 0u;
     }
     if constexpr (K8) {
       uint32_t top = 0u;
@@ -615,19 +635,28 @@ __device__ __forceinline__ void append_row(const PageAttnArgs& a, const RowKeys&
   }
 }
 
-// Joins the warps' states of head h, channel ch.
-__device__ __forceinline__ void join_warps(const float* mo, const float* ml, int h, int ch, float& M,
-                                           float& L, float& O) {
-  M = -INFINITY;
+// Joins the warps' states: put(h, channel, M, L, O) for every head, thread t taking channel t.
+static_assert(kPaThreads == kD, "a thread per channel");
+template <typename Put>
+__device__ __forceinline__ void join_warps(const float* mo, const float* ml, int gs, Put put) {
+  const int ch = threadIdx.x;
+#pragma unroll 4
+  for (int h = 0; h < gs; ++h) {
+    float m[kPaWarps], M = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kPaWarps; ++w) M = fmaxf(M, ml[(w * kMaxGroup + h) * 2]);
-  const float mu = M == -INFINITY ? 0.f : M;
-  L = O = 0.f;
+    for (int w = 0; w < kPaWarps; ++w) {
+      m[w] = ml[(w * kMaxGroup + h) * 2];
+      M = fmaxf(M, m[w]);
+    }
+    const float mu = M == -INFINITY ? 0.f : M;
+    float L = 0.f, O = 0.f;
 #pragma unroll
-  for (int w = 0; w < kPaWarps; ++w) {
-    const float f = exp2f(ml[(w * kMaxGroup + h) * 2] - mu);
-    L = fmaf(f, ml[(w * kMaxGroup + h) * 2 + 1], L);
-    O = fmaf(f, mo[((size_t)w * kMaxGroup + h) * kD + ch], O);
+    for (int w = 0; w < kPaWarps; ++w) {
+      const float f = ex2(m[w] - mu);
+      L = fmaf(f, ml[(w * kMaxGroup + h) * 2 + 1], L);
+      O = fmaf(f, mo[((size_t)w * kMaxGroup + h) * kD + ch], O);
+    }
+    put(h, ch, M, L, O);
   }
 }
 
@@ -674,15 +703,12 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
     if (!kList && a.k_new != nullptr && off + take == ub && rk.n > 0) append_row<K8>(a, rk, b);
     __syncthreads();  // the new row is visible; the previous segment's state has been read
     const size_t head0 = (size_t)bt * a.Hq + (size_t)r * gs;
-    page_segment<K8, kList, kPair, kPaStages>(a, rk, a.q + head0 * kD, gs, off * kUnitKeys,
+    page_segment<K8, kList, kPair, kPaStages, K8>(a, rk, a.q + head0 * kD, gs, off * kUnitKeys,
                             min(rk.n, (off + take) * kUnitKeys),
                             reinterpret_cast<char*>(pa_smem), mo, ml);
     const bool whole = off == 0 && take == ub;
     const size_t slot = 2 * (size_t)c + (off == 0 ? 1 : 0);
-    for (int i = tid; i < gs * kD; i += kPaThreads) {
-      const int h = i / kD, ch = i % kD;
-      float M, L, O;
-      join_warps(mo, ml, h, ch, M, L, O);
+    join_warps(mo, ml, gs, [&](int h, int ch, float M, float L, float O) {
       if (whole) {
         put_out(a, head0 + h, ch, M, L, O);
       } else {
@@ -692,7 +718,7 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
           a.part_ml[(slot * gs + h) * 2 + 1] = L;
         }
       }
-    }
+    });
     u += take;
     if (u >= end) break;
     ++row;
@@ -736,20 +762,20 @@ __global__ void __launch_bounds__(kPaThreads, kPcCtasPerSm) page_cluster_kernel(
   if (!kList && a.k_new != nullptr && k0 < k1 && k1 == rk.n) append_row<K8>(a, rk, b);
   __syncthreads();
   const size_t head0 = (size_t)bt * a.Hq + (size_t)r * gs;
-  page_segment<K8, kList, kPair, kPcStages>(a, rk, a.q + head0 * kD, gs, k0, k1,
+  page_segment<K8, kList, kPair, kPcStages, true>(a, rk, a.q + head0 * kD, gs, k0, k1,
                                             reinterpret_cast<char*>(pa_smem), mo, ml);
   cluster_wait();
-  for (int i = tid; i < gs * kD; i += kPaThreads) {
-    const int h = i / kD, to = i / part;
-    float M, L, O;
-    join_warps(mo, ml, h, i % kD, M, L, O);
+  const float per_part = 1.f / (float)part;
+  join_warps(mo, ml, gs, [&](int h, int ch, float M, float L, float O) {
+    // i / part: i + 1/2 is no nearer to a multiple of part than 1/2, so the rounding is harmless.
+    const int i = h * kD + ch, to = (int)(((float)i + 0.5f) * per_part);
     *cl.map_shared_rank(inbox + rank * part + (i - to * part), to) = O;
-    if (i % kD < cs) {  // (M, L) of the head, once to each rank
-      float* x = cl.map_shared_rank(inbox_ml + (rank * kMaxGroup + h) * 2, i % kD);
+    if (ch < cs) {  // (M, L) of the head, once to each rank
+      float* x = cl.map_shared_rank(inbox_ml + (rank * kMaxGroup + h) * 2, ch);
       x[0] = M;
       x[1] = L;
     }
-  }
+  });
   cluster_sync_all();  // every rank's share has arrived; no remote access follows
   const int n = min(part, gs * kD - rank * part);
   for (int j = tid; j < n; j += kPaThreads) {
@@ -765,7 +791,7 @@ __global__ void __launch_bounds__(kPaThreads, kPcCtasPerSm) page_cluster_kernel(
 #pragma unroll
     for (int c = 0; c < kPaMaxCluster; ++c) {
       if (c < cs) {
-        const float f = exp2f(m[c] - mu);
+        const float f = ex2(m[c] - mu);
         L = fmaf(f, inbox_ml[(c * kMaxGroup + h) * 2 + 1], L);
         O = fmaf(f, inbox[c * part + j], O);
       }
