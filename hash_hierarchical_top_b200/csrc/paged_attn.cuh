@@ -32,9 +32,12 @@
 //
 // 8-bit cache: e4m3 numbers become f16 exactly. Q is scaled by a power of two per head so that
 // its largest channel is in [2^14, 2^15): bf16 queries are then exact in f16 down to 2^-38 of
-// the largest channel (smaller ones round to 0). The key's exponent multiplies its logit; the
-// value's exponent goes into the weight, relative to the warp's running largest one (E_run), and
-// 2^14 more keeps small weights out of f16's subnormal range.
+// the largest channel (smaller ones round to 0). The key's exponent multiplies its logit; the value's exponent goes into the
+// weight, relative to the warp's running largest one (E_run), and 2^14 more keeps small weights
+// out of f16's subnormal range: with value exponents within kPaSpread of one another, a weight is
+// off by 2^-22 of itself or 2^-25 of the largest one. A warp that meets anything else (value
+// exponents further apart) has its keys taken again in plain fp32 (warp_fp32), at about a tenth of
+// the rate.
 //
 // Split of the work: the rows' keys, in units of kUnitKeys, are laid end to end and divided
 // evenly over the CTAs (three per SM), whatever the lengths; a CTA's share covers the end of one
@@ -245,14 +248,191 @@ __device__ __forceinline__ uint32_t row_of(const PageAttnArgs& a, const RowKeys&
 constexpr int kPaTile = 4096;
 constexpr int kPaStage = 2 * kPaTile + 256;
 
+// Row `row` (over all sequences and tokens), sequence b: where its keys are.
+template <bool kList>
+__device__ __forceinline__ RowKeys row_keys(const PageAttnArgs& a, int row, int b) {
+  const int bt = row / a.Gs, r = row - bt * a.Gs;
+  RowKeys rk;
+  rk.pages = a.page_table + (size_t)b * a.maxp;
+  rk.g = (uint32_t)(a.kv_div == 1 ? r : r / a.kv_div);
+  rk.limit = dense_len(a, b);
+  if (kList && a.q_pos != nullptr) rk.limit = min(rk.limit - 1, a.q_pos[bt]) + 1;
+  rk.blocks = kList ? a.blocks + (size_t)row * a.m_max : nullptr;
+  rk.n = kList ? min(max(a.block_count[row], 0), a.m_max) * a.P : rk.limit;
+  if (!kList && threadIdx.x == 0 && a.seq_len[b] > a.maxp * a.P) flag_status(kStatusBadToken);
+  return rk;
+}
+
+// Binades that the value exponents of one warp's keys may span in f16 weights.
+constexpr uint32_t kPaSpread = 14;
+
+// The exact way for keys that f16 operands do not hold: plain fp32, on the warp's keys
+// k0 .. k0 + 31, then those `step` on, below k1. Rare, so that it is no part of the kernels' loops.
+
+// The cache row of slot j.
+template <bool kList>
+__device__ __forceinline__ uint32_t row_at(const PageAttnArgs& a, const RowKeys& rk, int j, int k1) {
+  int block = load_block<kList>(a, rk, j, k1);
+  const int page = load_page<kList>(a, rk, block, j, k1);
+  return row_of(a, rk, j, block, page);
+}
+
+// Whether f16 does not hold the warp's keys. page_segment asks where it has seen exponents far apart;
+// it does not tell a row of zeros, which has the smallest exponent byte and adds nothing under any
+// scale, from values that small.
+template <bool kList>
+__device__ __forceinline__ bool warp_far(const PageAttnArgs& a, const RowKeys& rk, int k0, int step,
+                                         int k1) {
+  const int lane = threadIdx.x & 31;
+  uint32_t low = 255u, high = 0u;
+#pragma unroll 1
+  for (int s0 = k0; s0 < k1; s0 += step) {
+    const uint32_t row = row_at<kList>(a, rk, s0 + lane, k1);
+    if (row == kNoRow) continue;
+    const uint32_t x = a.v_exp[row];
+    uint32_t any = 0u;
+    if (x <= kExpMin) {
+      const uint4* v = reinterpret_cast<const uint4*>(a.v) + (size_t)row * (kD / 16);
+      for (int c = 0; c < kD / 16; ++c) any |= v[c].x | v[c].y | v[c].z | v[c].w;
+    }
+    if (x > kExpMin || (any & 0x7f7f7f7fu) != 0u) low = min(low, x);
+    high = max(high, x);
+  }
+  low = __reduce_min_sync(kFull, low);
+  high = __reduce_max_sync(kFull, high);
+  return high > low + kPaSpread;
+}
+
+// Attention of up to NH heads q[n][d] over the warp's keys: a lane has the channels 4 lane + {0..3} of
+// o; maximum m (log2 units) and sum l of the weights. 8 keys are summed before they join the sums.
+template <bool kList, int NH>
+__device__ __forceinline__ void warp_fp32(const PageAttnArgs& a, const RowKeys& rk, const uint16_t* q,
+                                          int n, int k0, int step, int k1, float4 (&o)[NH],
+                                          float (&m)[NH], float (&l)[NH]) {
+  constexpr int N = 8;
+  const int lane = threadIdx.x & 31;
+  float4 qf[NH];
+#pragma unroll
+  for (int h = 0; h < NH; ++h) {
+    qf[h] = bf16x4_to_f4(*reinterpret_cast<const uint2*>(q + (size_t)min(h, n - 1) * kD + 4 * lane));
+    o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+    m[h] = -INFINITY;
+    l[h] = 0.f;
+  }
+  // Four e4m3 channels times 2^(x - 127).
+  auto channels = [](uint32_t w, float s) {
+    uint32_t lo, hi;
+    e4m3x4_to_f16x2(w, lo, hi);
+    const float2 x = f16x2_to_f2(lo), y = f16x2_to_f2(hi);
+    return make_float4(x.x * s, x.y * s, y.x * s, y.y * s);
+  };
+#pragma unroll 1
+  for (int s0 = k0; s0 < k1; s0 += step) {
+    const uint32_t row = row_at<kList>(a, rk, s0 + lane, k1);
+    const unsigned held = __ballot_sync(kFull, row != kNoRow);
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32; r0 += N) {
+      if ((held >> r0 & ((1u << N) - 1u)) == 0u) continue;
+      uint32_t kw[N], vw[N];
+      float ks[N], vs[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const uint32_t r = __shfl_sync(kFull, row, r0 + i);
+        const bool ok = r != kNoRow;
+        const size_t at = ok ? r : 0;
+        kw[i] = ok ? reinterpret_cast<const uint32_t*>(a.k)[at * (kD / 4) + lane] : 0u;
+        vw[i] = ok ? reinterpret_cast<const uint32_t*>(a.v)[at * (kD / 4) + lane] : 0u;
+        ks[i] = ok ? exp_scale(a.k_exp[at]) : 0.f;
+        vs[i] = ok ? exp_scale(a.v_exp[at]) : 0.f;
+      }
+#pragma unroll
+      for (int h = 0; h < NH; ++h) {
+        if (h >= n) break;
+        float x[N], top = m[h];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float4 k = channels(kw[i], ks[i]);
+          x[i] = fmaf(qf[h].x, k.x, fmaf(qf[h].y, k.y, fmaf(qf[h].z, k.z, qf[h].w * k.w)));
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          x[i] = warp_sum(x[i]) * a.scale_log2;
+          if (!(held >> (r0 + i) & 1u)) x[i] = -INFINITY;
+          top = fmaxf(top, x[i]);
+        }
+        const float mu = top == -INFINITY ? 0.f : top, corr = ex2(m[h] - mu);
+        m[h] = top;
+        float sum = 0.f;
+        float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float w = ex2(x[i] - mu);
+          const float4 v = channels(vw[i], vs[i]);
+          sum += w;
+          t.x = fmaf(w, v.x, t.x);
+          t.y = fmaf(w, v.y, t.y);
+          t.z = fmaf(w, v.z, t.z);
+          t.w = fmaf(w, v.w, t.w);
+        }
+        l[h] = fmaf(l[h], corr, sum);
+        o[h].x = fmaf(o[h].x, corr, t.x);
+        o[h].y = fmaf(o[h].y, corr, t.y);
+        o[h].z = fmaf(o[h].z, corr, t.z);
+        o[h].w = fmaf(o[h].w, corr, t.w);
+      }
+    }
+  }
+}
+
+// The same of a warp's part of keys [k0, k1) of a row, as page_segment deals them out.
+template <bool kList>
+__device__ __forceinline__ bool segment_far(const PageAttnArgs& a, int row, int b, int k0, int k1) {
+  const RowKeys rk = row_keys<kList>(a, row, b);
+  return warp_far<kList>(a, rk, k0 + (threadIdx.x & ~31u), kPaThreads, min(k1, rk.n));
+}
+template <bool kList>
+__device__ __forceinline__ void segment_fp32(const PageAttnArgs& a, int row, int b, int k0, int k1,
+                                             float* mo, float* ml) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gs = a.Hq / a.Gs;
+  const RowKeys rk = row_keys<kList>(a, row, b);
+  constexpr int NH = 4;
+  mo += (size_t)warp * kMaxGroup * kD + 4 * lane;
+  ml += warp * kMaxGroup * 2;
+#pragma unroll 1
+  for (int h0 = 0; h0 < gs; h0 += NH) {
+    float4 o[NH];
+    float m[NH], l[NH];
+    warp_fp32<kList, NH>(a, rk, a.q + ((size_t)row * gs + h0) * kD, gs - h0, k0 + 32 * warp,
+                         kPaThreads, min(k1, rk.n), o, m, l);
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      if (h0 + h >= gs) break;
+      *reinterpret_cast<float4*>(mo + (h0 + h) * kD) = o[h];
+      if (lane == 0) {
+        ml[2 * (h0 + h)] = m[h];
+        ml[2 * (h0 + h) + 1] = l[h];
+      }
+    }
+  }
+}
+// A cluster's warp whose exponents page_segment found far apart: looks, and replaces its state. Not
+// inlined, and given the row's place only, to stay out of page_segment's registers.
+template <bool kList>
+__device__ __noinline__ void page_segment_fp32(PageAttnArgs a, int row, int b, int k0, int k1,
+                                               float* mo, float* ml) {
+  if (!segment_far<kList>(a, row, b, k0, k1)) return;
+  __syncwarp();  // the state that is replaced has been written
+  segment_fp32<kList>(a, row, b, k0, k1, mo, ml);
+}
+
 // Keys [k0, k1) of a row, over the CTA's warps: the state of every head is left in shared
-// memory (mo [warps][8][d], ml [warps][8][2], which reuse the rings). Ends with the state of
-// all warps written (a barrier).
+// memory (mo [warps][8][d], ml [warps][8][2], which reuse the rings). True where the warp's exponents may
+// be too far apart for its sums to hold (warp_far tells, warp_fp32 mends). A barrier has to follow.
 // kSoon issues the query loads before the first keys are located instead of after their copies:
 // a cluster's few steps gain the latency (517 keys 5.87 -> 5.72 us, lists of 64 blocks 12.85 ->
 // 12.63); the shares of bf16 rows lose 1% to the registers it holds, so that they load late.
 template <bool K8, bool kList, bool kPair, int NS, bool kSoon>
-__device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKeys& rk,
+__device__ __forceinline__ bool page_segment(const PageAttnArgs& a, const RowKeys& rk,
                                              const uint16_t* q, int gs, int k0, int k1,
                                              char* smem, float* mo, float* ml) {
   constexpr int S = K8 ? 32 : 16;       // keys of a warp's step
@@ -342,6 +522,9 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
   // logit: logit = hs * product in log2 units, hs > 0 (a scale of 0 becomes the smallest number).
   if constexpr (!kSoon) load_q();
   float hs = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
+  // 8-bit: the smallest exponent byte of this lane's values, less 1 (a missing row's 0 becomes the
+  // largest).
+  uint32_t x_low = 0xffffffffu;
   {
     const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
 #pragma unroll
@@ -431,6 +614,7 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
     uint32_t e_new = e_run;
     if constexpr (K8) {
       e_new = max(e_run, __reduce_max_sync(kFull, xv));
+      x_low = min(x_low, xv - 1u);
       const uint32_t mine = xk << 23 | (uint32_t)max(127 + 14 + (int)xv - (int)e_new, 0) << 7;
 #pragma unroll
       for (int m = 0; m < NM; ++m)
@@ -533,6 +717,8 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
   cp_async_wait<0>();
   __syncthreads();  // every warp is done with its ring: mo and ml lie over them
 
+  float* mw = mo + (size_t)warp * kMaxGroup * kD;
+  float* mlw = ml + warp * kMaxGroup * 2;
 #pragma unroll
   for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -540,7 +726,6 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
   // oacc[i]: channel c0 (elements 0, 1) and c1 (2, 3) of the columns 2tq, 2tq + 1.
   // 8-bit: 2^-14 and the running exponent, one after the other (2^(e_run - 141) may be subnormal).
   const float os = K8 ? 6.103515625e-05f : 1.f, oe = K8 ? exp_scale(e_run) : 1.f;
-  float* mw = mo + (size_t)warp * kMaxGroup * kD;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if constexpr (kPair) {  // column c + 4 is the second part of column c
@@ -558,11 +743,12 @@ __device__ __forceinline__ void page_segment(const PageAttnArgs& a, const RowKey
   if (gq == 0) {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      ml[(warp * kMaxGroup + 2 * tq + e) * 2] = m_run[e] * hse[e];  // in log2 units
-      ml[(warp * kMaxGroup + 2 * tq + e) * 2 + 1] = l_run[e];
+      mlw[(2 * tq + e) * 2] = m_run[e] * hse[e];  // in log2 units
+      mlw[(2 * tq + e) * 2 + 1] = l_run[e];
     }
   }
-  __syncthreads();
+  if constexpr (!K8) return false;
+  return __any_sync(kFull, e_run > min(x_low, 255u) + 1u + kPaSpread || x_low < (uint32_t)kExpMin);
 }
 
 // Writes output channel c of query head `head` (and, for c == 0, its log of the weights' sum).
@@ -596,21 +782,6 @@ constexpr int kPcShares = kMaxGroup * kD + kPaMaxCluster;                       
 constexpr int kPcInbox = kPcShares + 2 * kPaMaxCluster * kMaxGroup;
 inline size_t page_cluster_smem() {
   return (size_t)kPaWarps * kPcStages * kPaStage + (size_t)kPcInbox * 4;
-}
-
-// Row `row` (over all sequences and tokens), sequence b: where its keys are.
-template <bool kList>
-__device__ __forceinline__ RowKeys row_keys(const PageAttnArgs& a, int row, int b) {
-  const int bt = row / a.Gs, r = row - bt * a.Gs;
-  RowKeys rk;
-  rk.pages = a.page_table + (size_t)b * a.maxp;
-  rk.g = (uint32_t)(a.kv_div == 1 ? r : r / a.kv_div);
-  rk.limit = dense_len(a, b);
-  if (kList && a.q_pos != nullptr) rk.limit = min(rk.limit - 1, a.q_pos[bt]) + 1;
-  rk.blocks = kList ? a.blocks + (size_t)row * a.m_max : nullptr;
-  rk.n = kList ? min(max(a.block_count[row], 0), a.m_max) * a.P : rk.limit;
-  if (!kList && threadIdx.x == 0 && a.seq_len[b] > a.maxp * a.P) flag_status(kStatusBadToken);
-  return rk;
 }
 
 // Dense: writes the newest row (position rk.n - 1) of sequence b into the cache; by the CTA that
@@ -660,7 +831,89 @@ __device__ __forceinline__ void join_warps(const float* mo, const float* ml, int
   }
 }
 
-// Even shares of all rows' keys (see the head of this file).
+// A CTA's even share of all rows' keys (see the head of this file), of which units [off, off + take())
+// of row `row` (over all sequences and tokens; sequence b) come next.
+struct Share {
+  int u, end, row, b, off, ub;  // units [u, end) are left; ub: units of the row
+  __device__ __forceinline__ int take() const { return min(end - u, ub - off); }
+};
+// False: this CTA has no share. Block-wide; sh: 40 ints.
+template <bool kList>
+__device__ __forceinline__ bool share_start(const PageAttnArgs& a, int* sh, Share& s) {
+  const int c = blockIdx.x;
+  int total;
+  if (kList) {
+    s.ub = units_of(a.m_max * a.P);
+    total = a.B * a.T * a.Gs * s.ub;
+  } else {
+    const UnitPlace p = dense_place(a, sh, [&](int all) {
+      return min(share_begin(c, all, share_count(a, all)), all - 1);
+    });
+    total = p.total;
+    s.b = p.b;
+    s.off = p.before;
+  }
+  const int n = share_count(a, total);
+  if (c >= n) return false;
+  s.u = share_begin(c, total, n);
+  s.end = share_begin(c + 1, total, n);
+  if (kList) {
+    s.row = s.u / s.ub;
+    s.off = s.u - s.row * s.ub;
+    s.b = s.row / a.Gs / a.T;
+  } else {
+    s.ub = units_of(dense_len(a, s.b));
+    s.row = s.b * a.Gs + (s.u - s.off) / s.ub;
+    s.off = (s.u - s.off) % s.ub;
+  }
+  return true;
+}
+// On to the next row; false at the share's end.
+template <bool kList>
+__device__ __forceinline__ bool share_next(const PageAttnArgs& a, Share& s) {
+  s.u += s.take();
+  if (s.u >= s.end) return false;
+  ++s.row;
+  s.off = 0;
+  s.b = kList ? s.row / a.Gs / a.T : s.row / a.Gs;
+  if (!kList) s.ub = units_of(dense_len(a, s.b));
+  return true;
+}
+// Writes what the CTA's warps have of the share's part: the outputs of a whole row, else a partial.
+__device__ __forceinline__ void put_part(const PageAttnArgs& a, const Share& s, const float* mo,
+                                         const float* ml) {
+  const int gs = a.Hq / a.Gs;
+  const bool whole = s.off == 0 && s.take() == s.ub;
+  const size_t slot = 2 * (size_t)blockIdx.x + (s.off == 0 ? 1 : 0);
+  join_warps(mo, ml, gs, [&](int h, int ch, float M, float L, float O) {
+    if (whole) {
+      put_out(a, (size_t)s.row * gs + h, ch, M, L, O);
+    } else {
+      a.part_o[(slot * gs + h) * kD + ch] = O;
+      if (ch == 0) {
+        a.part_ml[(slot * gs + h) * 2] = M;
+        a.part_ml[(slot * gs + h) * 2 + 1] = L;
+      }
+    }
+  });
+}
+
+// The CTA's share once more, where f16 operands do not hold a part of it: the last thing that the
+// kernel does, so that its loop keeps nothing in registers for the call (a call per part made lists
+// of 64 queries 4% slower; so did arguments by reference).
+template <bool kList>
+__device__ __noinline__ void page_share_fp32(PageAttnArgs a, int* sh, float* mo, float* ml) {
+  Share s;
+  if (!share_start<kList>(a, sh, s)) return;
+  do {
+    const int k0 = s.off * kUnitKeys, k1 = k0 + s.take() * kUnitKeys;
+    if (!__syncthreads_or(segment_far<kList>(a, s.row, s.b, k0, k1))) continue;
+    segment_fp32<kList>(a, s.row, s.b, k0, k1, mo, ml);
+    __syncthreads();
+    put_part(a, s, mo, ml);
+  } while (share_next<kList>(a, s));
+}
+
 template <bool K8, bool kList, bool kPair>
 __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(PageAttnArgs a) {
   pdl_wait();
@@ -668,66 +921,24 @@ __global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm) page_attn_kernel(Pag
   __shared__ int sh[40];
   float* mo = reinterpret_cast<float*>(pa_smem);
   float* ml = mo + kPaWarps * kMaxGroup * kD;
-  const int tid = threadIdx.x, gs = a.Hq / a.Gs;
+  const int gs = a.Hq / a.Gs;
   pdl_trigger();  // page_join_kernel waits for this grid's end before it reads the partials
-  int total, b, off, row, ub;  // row: over all sequences and tokens; ub: its units
-  const int c = blockIdx.x;
-  if (kList) {
-    ub = units_of(a.m_max * a.P);
-    total = a.B * a.T * a.Gs * ub;
-  } else {
-    const UnitPlace p = dense_place(a, sh, [&](int all) {
-      return min(share_begin(c, all, share_count(a, all)), all - 1);
-    });
-    total = p.total;
-    b = p.b;
-    off = p.before;
-  }
-  const int n = share_count(a, total);
-  if (c >= n) return;
-  int u = share_begin(c, total, n);
-  const int end = share_begin(c + 1, total, n);
-  if (kList) {
-    row = u / ub;
-    off = u - row * ub;
-  } else {
-    ub = units_of(dense_len(a, b));
-    row = b * a.Gs + (u - off) / ub;
-    off = (u - off) % ub;
-  }
-  while (true) {
-    const int take = min(end - u, ub - off);
-    const int bt = row / a.Gs, r = row - bt * a.Gs;
-    if (kList) b = bt / a.T;
-    const RowKeys rk = row_keys<kList>(a, row, b);
-    if (!kList && a.k_new != nullptr && off + take == ub && rk.n > 0) append_row<K8>(a, rk, b);
+  Share s;
+  if (!share_start<kList>(a, sh, s)) return;
+  bool far = false;
+  do {
+    const RowKeys rk = row_keys<kList>(a, s.row, s.b);
+    const int take = s.take();
+    if (!kList && a.k_new != nullptr && s.off + take == s.ub && rk.n > 0) append_row<K8>(a, rk, s.b);
     __syncthreads();  // the new row is visible; the previous segment's state has been read
-    const size_t head0 = (size_t)bt * a.Hq + (size_t)r * gs;
-    page_segment<K8, kList, kPair, kPaStages, K8>(a, rk, a.q + head0 * kD, gs, off * kUnitKeys,
-                            min(rk.n, (off + take) * kUnitKeys),
-                            reinterpret_cast<char*>(pa_smem), mo, ml);
-    const bool whole = off == 0 && take == ub;
-    const size_t slot = 2 * (size_t)c + (off == 0 ? 1 : 0);
-    join_warps(mo, ml, gs, [&](int h, int ch, float M, float L, float O) {
-      if (whole) {
-        put_out(a, head0 + h, ch, M, L, O);
-      } else {
-        a.part_o[(slot * gs + h) * kD + ch] = O;
-        if (ch == 0) {
-          a.part_ml[(slot * gs + h) * 2] = M;
-          a.part_ml[(slot * gs + h) * 2 + 1] = L;
-        }
-      }
-    });
-    u += take;
-    if (u >= end) break;
-    ++row;
-    off = 0;
-    if (!kList) {
-      b = row / a.Gs;
-      ub = units_of(dense_len(a, b));
-    }
-  }
+    far |= page_segment<K8, kList, kPair, kPaStages, K8>(
+        a, rk, a.q + (size_t)s.row * gs * kD, gs, s.off * kUnitKeys,
+        min(rk.n, (s.off + take) * kUnitKeys), reinterpret_cast<char*>(pa_smem), mo, ml);
+    __syncthreads();
+    put_part(a, s, mo, ml);
+  } while (share_next<kList>(a, s));
+  if constexpr (K8)
+    if (__syncthreads_or(far)) page_share_fp32<kList>(a, sh, mo, ml);
 }
 
 // One cluster per row: its CTAs take equal parts of the row's keys. Rank r writes the r-th part of
@@ -762,8 +973,10 @@ __global__ void __launch_bounds__(kPaThreads, kPcCtasPerSm) page_cluster_kernel(
   if (!kList && a.k_new != nullptr && k0 < k1 && k1 == rk.n) append_row<K8>(a, rk, b);
   __syncthreads();
   const size_t head0 = (size_t)bt * a.Hq + (size_t)r * gs;
-  page_segment<K8, kList, kPair, kPcStages, true>(a, rk, a.q + head0 * kD, gs, k0, k1,
-                                            reinterpret_cast<char*>(pa_smem), mo, ml);
+  if (page_segment<K8, kList, kPair, kPcStages, true>(a, rk, a.q + head0 * kD, gs, k0, k1,
+                                                      reinterpret_cast<char*>(pa_smem), mo, ml))
+    page_segment_fp32<kList>(a, row, b, k0, k1, mo, ml);
+  __syncthreads();
   cluster_wait();
   const float per_part = 1.f / (float)part;
   join_warps(mo, ml, gs, [&](int h, int ch, float M, float L, float O) {

@@ -1,0 +1,178 @@
+"""Attention over an 8-bit cache whose exponents lie far apart: legal inputs that 16-bit matrix
+operands do not hold, against the float64 definition.
+
+Tolerances are those of page_helpers, with a logit's error taken key by key (a key of negligible
+weight may have a long, and so less exact, product): a weight w_j is off by w_j ds_j, and so
+  |o - o_ref| <= sum_j w_j ds_j |v_j| + |o_ref| sum_j w_j ds_j + (2^-21 + sums) sum_j w_j |v_j|
+                 + 2^-25 sum_j |v_j|     (weights normalised to a sum of 1, the last of them to a
+                                          largest weight of 1, over their sum)
+where the last term is what a weight loses below the matrix operands' range, relative to the largest.
+"""
+import math
+
+import pytest
+import torch
+
+from hash_hierarchical_top_b200 import build, hhr
+from page_helpers import D, Paged, check, status_ok
+
+pytestmark = pytest.mark.gpu
+SCALE = 1.0 / math.sqrt(D)
+
+
+def ref_rows(q, k, v, scale):
+    """(o, lse, tolerances) of q [h, D] over rows k, v [n, D] in float64."""
+    q, n = q.double(), len(k)
+    s = scale * (q @ k.T)
+    ds = 2.0 ** -19 * abs(scale) * (q.abs() @ k.abs().T) + 2.0 ** -22 * s.abs()
+    top = s.amax(1, keepdim=True)
+    w = torch.exp(s - top)
+    total = w.sum(1, keepdim=True)
+    o, lse = (w @ v) / total, (top + total.log())[:, 0]
+    off = (w * ds).sum(1, keepdim=True) / total
+    sums = (n / 128 + 64) * 2.0 ** -22
+    tol = ((w * ds) @ v.abs() / total + o.abs() * off + (2.0 ** -21 + sums) * (w @ v.abs()) / total +
+           2.0 ** -25 * v.abs().sum(0) / total)
+    # fp32 results below 2^-126 have an absolute step of 2^-149.
+    return o, lse, tol + 2.0 ** -146, off[:, 0] + sums + 2.0 ** -22 * lse.abs()
+
+
+def run(c, q, path, scale=SCALE):
+    """Outputs [h, D] and lse [h] per KV head of a single sequence, by a dense call or a list of all
+    its pages."""
+    out = torch.full((1, c.G * c.gs, D), math.nan, device="cuda")
+    lse = torch.full((1, c.G * c.gs), math.nan, device="cuda")
+    if path == "dense":
+        ws = torch.full((hhr.hhr_paged_attn_workspace_bytes(c.d),), 0xff, dtype=torch.uint8, device="cuda")
+        hhr.hhr_paged_attn(c.d, q, None, None, c.k, c.v, c.k_exp, c.v_exp, c.pt, c.seq_len, scale, out, ws,
+                           lse=lse)
+    else:
+        n = -(-c.lens[0] // c.P)
+        blocks = torch.arange(n, dtype=torch.int32, device="cuda").expand(1, 1, c.G, n).contiguous()
+        count = torch.full((1, 1, c.G), n, dtype=torch.int32, device="cuda")
+        ws = torch.full((hhr.hhr_block_attn_workspace_bytes(c.d, 1, n),), 0xff, dtype=torch.uint8,
+                        device="cuda")
+        hhr.hhr_block_attn(c.d, q[:, None], c.k, c.v, c.k_exp, c.v_exp, c.pt, c.seq_len, None, blocks, count,
+                           scale, out[:, None], ws, lse=lse[:, None])
+    status_ok()
+    return out[0], lse[0]
+
+
+def check_all(c, q, out, lse, scale=SCALE):
+    pos = torch.arange(c.lens[0], device="cuda")
+    for g in range(c.G):
+        h = slice(g * c.gs, (g + 1) * c.gs)
+        o, l, to, tl = ref_rows(q[0, h], c.rows("k", 0, g, pos), c.rows("v", 0, g, pos), scale)
+        check(out[h], o, to, f"KV head {g}")
+        check(lse[h], l, tl, f"KV head {g} lse")
+
+
+def put(c, name, pos, values, exp):
+    """Row `pos` of sequence 0, all KV heads: e4m3 bytes {channel: byte}, zeros elsewhere."""
+    phys, slot = int(c.pt[0, pos // c.P]), pos % c.P
+    x, e = getattr(c, name), getattr(c, name + "_exp")
+    x[phys, :, slot] = 0
+    for ch, byte in values.items():
+        x[phys, :, slot, ch] = byte
+    e[phys, :, slot] = exp
+
+
+def against(c, q, pos, size):
+    """Key row `pos` becomes -size times the sum of its group's queries: little weight everywhere."""
+    from page_helpers import quantise_ref
+    phys, slot = int(c.pt[0, pos // c.P]), pos % c.P
+    x = -size * q[0].float().reshape(c.G, c.gs, D).sum(1)
+    b, e = quantise_ref(x.bfloat16())
+    c.k[phys, :, slot], c.k_exp[phys, :, slot] = b.cuda(), e.cuda()
+
+
+# Lengths that a cluster per row takes, and ones that are split evenly over all CTAs.
+PATHS = [("dense", 600), ("dense", 9001), ("list", 600), ("list", 20000)]
+
+
+@pytest.mark.parametrize("gap", [0, 8, 13, 14, 15, 17, 20, 24, 30, 34, 40, 60, 90, 126])
+@pytest.mark.parametrize("negligible", [True, False])
+@pytest.mark.parametrize("gs", [2, 5])
+@pytest.mark.parametrize("path,n", PATHS)
+def test_value_rows_of_larger_exponents(path, n, gs, negligible, gap):
+    """Two value rows far larger than the others, in one channel only, one of them among the first
+    keys: the other channels are the other keys' sums, whatever the large rows weigh."""
+    build.build()
+    c = Paged([n], 1, gs, 32, True, seed=100 + gap)
+    q = c.queries(1)
+    for pos in (1, n - 70):
+        if negligible:
+            against(c, q, pos, 3.0)
+        put(c, "v", pos, {9: 0x7e}, 120 + gap)            # 448 * 2^(gap - 7)
+    check_all(c, q, *run(c, q, path))
+
+
+@pytest.mark.parametrize("path,n", PATHS)
+@pytest.mark.parametrize("gap", [12, 14, 16, 25, 40, 105])
+def test_value_rows_of_smaller_exponents(path, n, gap):
+    """One key that nearly takes all, whose value row is far smaller than the others; in channels
+    that the others leave empty it is all there is."""
+    build.build()
+    c = Paged([n], 2, 4, 16, True, seed=200 + gap)
+    c.v[..., 64:] = torch.where(c.v_exp[..., None] == 255, c.v[..., 64:], torch.zeros_like(c.v[..., 64:]))
+    q = c.queries(1)
+    against(c, q, 37, -0.5)
+    put(c, "v", 37, {ch: 0x3a + ch % 7 for ch in range(D)}, max(10, 120 - gap))
+    check_all(c, q, *run(c, q, path))
+
+
+@pytest.mark.parametrize("weight", [3.0, 0.0])
+@pytest.mark.parametrize("path,n", PATHS)
+def test_an_infinite_value_acts_on_its_channel_only(path, n, weight):
+    """A value row with an infinity, as the append quantises it: 448 * 2^119 in that channel."""
+    build.build()
+    c = Paged([n], 2, 4, 32, True, seed=300)
+    q = c.queries(1)
+    new = torch.randn(1, 1, 2, D, device="cuda").bfloat16()
+    new[..., 77] = math.inf
+    i32 = lambda x: torch.tensor([x], dtype=torch.int32, device="cuda")
+    hhr.hhr_append_kv8(c.d, new.clone().nan_to_num(1.0, 1.0), new, i32(n - 1), i32(1), c.pt, c.k, c.v,
+                       c.k_exp, c.v_exp)
+    if weight:
+        against(c, q, n - 1, weight)
+    out, lse = run(c, q, path)
+    check_all(c, q, out, lse)
+    assert (out[:, 77] > 1e6).all() and (out[:, :77].abs() < 10).all()
+
+
+@pytest.mark.parametrize("path,n", PATHS)
+def test_value_rows_of_zeros(path, n):
+    """Rows of zeros (the smallest exponent byte, zeros of both signs) among ordinary ones, and one
+    row under the same byte that is not zero, in a channel of its own."""
+    build.build()
+    c = Paged([n], 1, 4, 32, True, seed=310)
+    q = c.queries(1)
+    for pos in range(0, n, 5):
+        put(c, "v", pos, {3: 0x80}, 10)
+    check_all(c, q, *run(c, q, path))
+    c.v[..., 5] = torch.where(c.v_exp == 255, c.v[..., 5], torch.zeros_like(c.v[..., 5]))
+    put(c, "v", 300, {5: 0x7e}, 10)
+    out, lse = run(c, q, path)
+    check_all(c, q, out, lse)
+    assert (out[:, 5] > 0).all()
+
+
+@pytest.mark.parametrize("path,n", PATHS)
+def test_nan_and_infinite_queries_act_on_their_heads_only(path, n):
+    """Beside an ordinary cache, and beside one that the wide range is needed for."""
+    build.build()
+    for far in (False, True):
+        c = Paged([n], 1, 4, 32, True, seed=700)
+        q = c.queries(1)
+        q[0, 1, 5] = math.nan
+        q[0, 2, 6] = math.inf
+        if far:
+            put(c, "v", 40, {9: 0x7e}, 200)
+        c.k[..., 6] = torch.where(c.k_exp == 255, c.k[..., 6], torch.full_like(c.k[..., 6], 0x38))
+        out, lse = run(c, q, path)
+        assert torch.isnan(out[1]).all() and torch.isnan(out[2]).all()
+        keep = [0, 3]
+        pos = torch.arange(n, device="cuda")
+        o, l, to, tl = ref_rows(q[0, keep], c.rows("k", 0, 0, pos), c.rows("v", 0, 0, pos), SCALE)
+        check(out[keep], o, to, "rest")
+        check(lse[keep], l, tl, "rest lse")
