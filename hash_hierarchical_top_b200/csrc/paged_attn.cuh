@@ -36,8 +36,8 @@
 // weight, relative to the warp's running largest one (E_run), and 2^14 more keeps small weights
 // out of f16's subnormal range: with value exponents within kPaSpread of one another, a weight is
 // off by 2^-22 of itself or 2^-25 of the largest one. A warp that meets anything else (value
-// exponents further apart) has its keys taken again in plain fp32 (warp_fp32), at about a tenth of
-// the rate.
+// exponents further apart, keys that would leave fp32 on the way to an ordinary logit) has
+// its keys taken again in plain fp32 (warp_fp32), at about a tenth of the rate.
 //
 // Split of the work: the rows' keys, in units of kUnitKeys, are laid end to end and divided
 // evenly over the CTAs (three per SM), whatever the lengths; a CTA's share covers the end of one
@@ -265,6 +265,8 @@ __device__ __forceinline__ RowKeys row_keys(const PageAttnArgs& a, int row, int 
 
 // Binades that the value exponents of one warp's keys may span in f16 weights.
 constexpr uint32_t kPaSpread = 14;
+// Largest exponent byte of a key whose f16 products stay in fp32: 128 of at most 2^15 448 2^96.
+constexpr uint32_t kPaKeyTop = 127 + 96;
 
 // The exact way for keys that f16 operands do not hold: plain fp32, on the warp's keys
 // k0 .. k0 + 31, then those `step` on, below k1. Rare, so that it is no part of the kernels' loops.
@@ -284,7 +286,7 @@ template <bool kList>
 __device__ __forceinline__ bool warp_far(const PageAttnArgs& a, const RowKeys& rk, int k0, int step,
                                          int k1) {
   const int lane = threadIdx.x & 31;
-  uint32_t low = 255u, high = 0u;
+  uint32_t low = 255u, high = 0u, key = 0u;
 #pragma unroll 1
   for (int s0 = k0; s0 < k1; s0 += step) {
     const uint32_t row = row_at<kList>(a, rk, s0 + lane, k1);
@@ -297,10 +299,11 @@ __device__ __forceinline__ bool warp_far(const PageAttnArgs& a, const RowKeys& r
     }
     if (x > kExpMin || (any & 0x7f7f7f7fu) != 0u) low = min(low, x);
     high = max(high, x);
+    key = max(key, (uint32_t)a.k_exp[row]);
   }
   low = __reduce_min_sync(kFull, low);
   high = __reduce_max_sync(kFull, high);
-  return high > low + kPaSpread;
+  return high > low + kPaSpread || __reduce_max_sync(kFull, key) > kPaKeyTop;
 }
 
 // Attention of up to NH heads q[n][d] over the warp's keys: a lane has the channels 4 lane + {0..3} of
@@ -523,8 +526,8 @@ __device__ __forceinline__ bool page_segment(const PageAttnArgs& a, const RowKey
   if constexpr (!kSoon) load_q();
   float hs = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
   // 8-bit: the smallest exponent byte of this lane's values, less 1 (a missing row's 0 becomes the
-  // largest).
-  uint32_t x_low = 0xffffffffu;
+  // largest), and the largest one of its keys.
+  uint32_t x_low = 0xffffffffu, x_key = 0u;
   {
     const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
 #pragma unroll
@@ -615,6 +618,7 @@ __device__ __forceinline__ bool page_segment(const PageAttnArgs& a, const RowKey
     if constexpr (K8) {
       e_new = max(e_run, __reduce_max_sync(kFull, xv));
       x_low = min(x_low, xv - 1u);
+      x_key = max(x_key, xk);
       const uint32_t mine = xk << 23 | (uint32_t)max(127 + 14 + (int)xv - (int)e_new, 0) << 7;
 #pragma unroll
       for (int m = 0; m < NM; ++m)
@@ -748,7 +752,8 @@ __device__ __forceinline__ bool page_segment(const PageAttnArgs& a, const RowKey
     }
   }
   if constexpr (!K8) return false;
-  return __any_sync(kFull, e_run > min(x_low, 255u) + 1u + kPaSpread || x_low < (uint32_t)kExpMin);
+  return __any_sync(kFull, e_run > min(x_low, 255u) + 1u + kPaSpread || x_low < (uint32_t)kExpMin ||
+                               x_key > kPaKeyTop);
 }
 
 // Writes output channel c of query head `head` (and, for c == 0, its log of the weights' sum).

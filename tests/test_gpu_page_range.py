@@ -1,5 +1,5 @@
-"""Attention over an 8-bit cache whose exponents lie far apart: legal inputs that 16-bit matrix
-operands do not hold, against the float64 definition.
+"""Attention over an 8-bit cache whose exponents lie far apart, and queries far from 1: legal inputs
+that 16-bit matrix operands do not hold, against the float64 definition.
 
 Tolerances are those of page_helpers, with a logit's error taken key by key (a key of negligible
 weight may have a long, and so less exact, product): a weight w_j is off by w_j ds_j, and so
@@ -155,6 +155,29 @@ def test_value_rows_of_zeros(path, n):
     out, lse = run(c, q, path)
     check_all(c, q, out, lse)
     assert (out[:, 5] > 0).all()
+
+
+@pytest.mark.parametrize("gs", [3, 8])
+@pytest.mark.parametrize("path,n", PATHS)
+@pytest.mark.parametrize("qs,ks", [(-60, 58), (-100, 100), (100, -100), (-60, 118)])
+def test_queries_and_keys_of_any_size(qs, ks, path, n, gs):
+    """Query times key in fp32's range, wherever its factors lie."""
+    build.build()
+    c = Paged([n], 1, gs, 32, True, seed=400, scale=2.0 ** ks)
+    q = (c.queries(1).float() * 2.0 ** qs).bfloat16()
+    # (Sizes whose logits pass what softmax tells apart are scaled down to it.)
+    scale = SCALE * 2.0 ** -max(0, qs + ks - 1)
+    out, lse = run(c, q, path, scale)
+    check_all(c, q, out, lse, scale)
+
+
+def test_a_large_key_where_every_query_is_zero():
+    build.build()
+    c = Paged([700], 1, 4, 32, True, seed=600)
+    q = c.queries(1)
+    q[..., 4] = 0
+    put(c, "k", 123, {4: 0x7e}, 246)                      # 448 * 2^119 where every query is 0
+    check_all(c, q, *run(c, q, "dense"))
 
 
 @pytest.mark.parametrize("path,n", PATHS)
