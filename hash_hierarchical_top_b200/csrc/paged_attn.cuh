@@ -31,12 +31,12 @@
 // us, 6.2-6.5 TB/s; 1 x 32K keys 30.3 us, of which the stream takes 21; 1 x 517 keys 5.7 us.
 //
 // 8-bit cache: e4m3 numbers become f16 exactly. Q is scaled by a power of two per head so that
-// its largest channel is in [2^14, 2^15): bf16 queries are then exact in f16 down to 2^-38 of
-// the largest channel (smaller ones round to 0). The key's exponent multiplies its logit; the value's exponent goes into the
+// its largest channel is in [2^14, 2^15): a bf16 query is then exact in f16 where its channels lie
+// within 31 binades. The key's exponent multiplies its logit; the value's exponent goes into the
 // weight, relative to the warp's running largest one (E_run), and 2^14 more keeps small weights
 // out of f16's subnormal range: with value exponents within kPaSpread of one another, a weight is
 // off by 2^-22 of itself or 2^-25 of the largest one. A warp that meets anything else (value
-// exponents further apart, keys that would leave fp32 on the way to an ordinary logit) has
+// exponents further apart, keys or queries that would leave fp32 on the way to an ordinary logit) has
 // its keys taken again in plain fp32 (warp_fp32), at about a tenth of the rate.
 //
 // Split of the work: the rows' keys, in units of kUnitKeys, are laid end to end and divided
@@ -267,8 +267,22 @@ __device__ __forceinline__ RowKeys row_keys(const PageAttnArgs& a, int row, int 
 constexpr uint32_t kPaSpread = 14;
 // Largest exponent byte of a key whose f16 products stay in fp32: 128 of at most 2^15 448 2^96.
 constexpr uint32_t kPaKeyTop = 127 + 96;
+// Whether f16 holds the queries of a head whose largest |channel| has the bf16 bits `top` and whose
+// smallest one that is not 0 has `low`: a head's logits are hs times products of channels times
+// 2^(141 - E), E the largest one's exponent field (141 for a head of zeros). Channels may be 31
+// binades apart (8 bits of each, down to 2^-24), and hs has to be a normal fp32 number.
+__device__ __forceinline__ uint32_t top_exponent(uint32_t top) {
+  return top == 0u ? 141u : max(top >> 7, 15u);
+}
+__device__ __forceinline__ float head_scale(const PageAttnArgs& a, uint32_t E) {
+  return fabsf(a.scale_log2) * __uint_as_float((E - 14u) << 23);
+}
+__device__ __forceinline__ bool queries_far(uint32_t top, uint32_t low, float hs) {
+  return top != 0u && ((top < 0x7f80u && (top >> 7) > (low >> 7) + 31u) ||
+                       !(hs >= 1.17549435e-38f && hs < INFINITY));
+}
 
-// The exact way for keys that f16 operands do not hold: plain fp32, on the warp's keys
+// The exact way for keys and queries that f16 operands do not hold: plain fp32, on the warp's keys
 // k0 .. k0 + 31, then those `step` on, below k1. Rare, so that it is no part of the kernels' loops.
 
 // The cache row of slot j.
@@ -279,13 +293,27 @@ __device__ __forceinline__ uint32_t row_at(const PageAttnArgs& a, const RowKeys&
   return row_of(a, rk, j, block, page);
 }
 
-// Whether f16 does not hold the warp's keys. page_segment asks where it has seen exponents far apart;
-// it does not tell a row of zeros, which has the smallest exponent byte and adds nothing under any
-// scale, from values that small.
+// Whether f16 does not hold the warp's keys under the queries q[gs][d]. page_segment asks where it has
+// seen exponents far apart; it does not tell a row of zeros, which has the smallest exponent byte and
+// adds nothing under any scale, from values that small.
 template <bool kList>
-__device__ __forceinline__ bool warp_far(const PageAttnArgs& a, const RowKeys& rk, int k0, int step,
-                                         int k1) {
+__device__ __forceinline__ bool warp_far(const PageAttnArgs& a, const RowKeys& rk, const uint16_t* q,
+                                         int gs, int k0, int step, int k1) {
   const int lane = threadIdx.x & 31;
+  bool far = false;
+  for (int h = 0; h < gs; ++h) {
+    const uint2 w = *reinterpret_cast<const uint2*>(q + (size_t)h * kD + 4 * lane);
+    uint32_t top = 0u, low = 0xffffu;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t x = ((i < 2 ? w.x : w.y) >> (16 * (i & 1))) & 0x7fffu;
+      top = max(top, x);
+      low = min(low, x - 1u);  // (0: out of the way)
+    }
+    top = __reduce_max_sync(kFull, top);
+    low = __reduce_min_sync(kFull, low);
+    far |= queries_far(top, low + 1u, head_scale(a, top_exponent(top)));
+  }
   uint32_t low = 255u, high = 0u, key = 0u;
 #pragma unroll 1
   for (int s0 = k0; s0 < k1; s0 += step) {
@@ -303,7 +331,7 @@ __device__ __forceinline__ bool warp_far(const PageAttnArgs& a, const RowKeys& r
   }
   low = __reduce_min_sync(kFull, low);
   high = __reduce_max_sync(kFull, high);
-  return high > low + kPaSpread || __reduce_max_sync(kFull, key) > kPaKeyTop;
+  return far || high > low + kPaSpread || __reduce_max_sync(kFull, key) > kPaKeyTop;
 }
 
 // Attention of up to NH heads q[n][d] over the warp's keys: a lane has the channels 4 lane + {0..3} of
@@ -390,8 +418,10 @@ __device__ __forceinline__ void warp_fp32(const PageAttnArgs& a, const RowKeys& 
 // The same of a warp's part of keys [k0, k1) of a row, as page_segment deals them out.
 template <bool kList>
 __device__ __forceinline__ bool segment_far(const PageAttnArgs& a, int row, int b, int k0, int k1) {
+  const int gs = a.Hq / a.Gs;
   const RowKeys rk = row_keys<kList>(a, row, b);
-  return warp_far<kList>(a, rk, k0 + (threadIdx.x & ~31u), kPaThreads, min(k1, rk.n));
+  return warp_far<kList>(a, rk, a.q + (size_t)row * gs * kD, gs, k0 + (threadIdx.x & ~31u),
+                         kPaThreads, min(k1, rk.n));
 }
 template <bool kList>
 __device__ __forceinline__ void segment_fp32(const PageAttnArgs& a, int row, int b, int k0, int k1,
@@ -522,11 +552,11 @@ __device__ __forceinline__ bool page_segment(const PageAttnArgs& a, const RowKey
   // zero). bf16: MMA i takes the channels 16i..16i+15 in order; 8-bit: k = 2tq, 2tq + 1, 2tq + 8,
   // 2tq + 9 are the channels 16i + 4tq + {0, 1, 2, 3}.
   // A negative scale goes into the queries' signs, so that the largest product is the largest
-  // logit: logit = hs * product in log2 units, hs > 0 (a scale of 0 becomes the smallest number).
+  // logit: logit = hs * product in log2 units, hs > 0.
   if constexpr (!kSoon) load_q();
   float hs = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
   // 8-bit: the smallest exponent byte of this lane's values, less 1 (a missing row's 0 becomes the
-  // largest), and the largest one of its keys.
+  // largest), and the largest one of its keys (255: queries that f16 does not hold).
   uint32_t x_low = 0xffffffffu, x_key = 0u;
   {
     const uint32_t sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
@@ -536,16 +566,26 @@ __device__ __forceinline__ bool page_segment(const PageAttnArgs& a, const RowKey
       qa[i][1] = hv ? qa[i][1] ^ sign : 0u;
     }
     if constexpr (K8) {
-      uint32_t top = 0u;
+      // Bits of the largest channel (of the column) and of the smallest that is not 0 (of the lane,
+      // less 1: a 0 becomes 0xffff).
+      uint32_t top2 = 0u, low2 = 0xffffffffu;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        top = max(max(top, max(qa[i][0] & 0x7fffu, (qa[i][0] >> 16) & 0x7fffu)),
-                  max(qa[i][1] & 0x7fffu, (qa[i][1] >> 16) & 0x7fffu));
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t mag = qa[i][e] & 0x7fff7fffu;
+          top2 = __vmaxu2(top2, mag);
+          low2 = __vminu2(low2, __vsub2(mag, 0x00010001u));
+        }
+      uint32_t top = max(top2 & 0xffffu, top2 >> 16);
+      const uint32_t low = min(low2 & 0xffffu, low2 >> 16) + 1u;
       top = max(top, __shfl_xor_sync(kFull, top, 1));
       top = max(top, __shfl_xor_sync(kFull, top, 2));
-      const uint32_t E = max(top >> 7, 15u);               // exponent field of the largest channel
+      const uint32_t E = top_exponent(top);
       const float up = __uint_as_float((268u - E) << 23);  // 2^(14 - (E - 127))
-      hs = fmaxf(hs * __uint_as_float((E - 14u) << 23), 1.17549435e-38f);
+      hs = head_scale(a, E);
+      if (queries_far(top, low, hs)) x_key = 255u;
+      hs = fmaxf(hs, 1.17549435e-38f);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         qa[i][0] = pack_f16(bf16_lo(qa[i][0]) * up, bf16_hi(qa[i][0]) * up);

@@ -159,7 +159,8 @@ def test_value_rows_of_zeros(path, n):
 
 @pytest.mark.parametrize("gs", [3, 8])
 @pytest.mark.parametrize("path,n", PATHS)
-@pytest.mark.parametrize("qs,ks", [(-60, 58), (-100, 100), (100, -100), (-60, 118)])
+@pytest.mark.parametrize("qs,ks", [(-60, 58), (-100, 100), (-112, 112), (-118, 116), (-124, 117), (100, -100),
+                                   (120, -115), (125, -117), (-60, 118)])
 def test_queries_and_keys_of_any_size(qs, ks, path, n, gs):
     """Query times key in fp32's range, wherever its factors lie."""
     build.build()
@@ -171,12 +172,30 @@ def test_queries_and_keys_of_any_size(qs, ks, path, n, gs):
     check_all(c, q, out, lse, scale)
 
 
-def test_a_large_key_where_every_query_is_zero():
+@pytest.mark.parametrize("path,n", PATHS)
+@pytest.mark.parametrize("spread", [20, 30, 32, 40, 100])
+def test_query_channels_of_very_different_sizes(path, n, spread):
+    """The largest query channel meets keys that are 0 there: the small channels decide."""
+    build.build()
+    c = Paged([n], 1, 4, 32, True, seed=500 + spread)
+    q = c.queries(1)
+    q[:, :, 11] = 1.5 * 2.0 ** spread
+    c.k[..., 11] = torch.where(c.k_exp == 255, c.k[..., 11], torch.zeros_like(c.k[..., 11]))
+    check_all(c, q, *run(c, q, path))
+
+
+@pytest.mark.parametrize("kind", ["zero queries", "one zero query", "one infinite key byte"])
+def test_zero_queries_and_single_large_keys(kind):
     build.build()
     c = Paged([700], 1, 4, 32, True, seed=600)
     q = c.queries(1)
-    q[..., 4] = 0
-    put(c, "k", 123, {4: 0x7e}, 246)                      # 448 * 2^119 where every query is 0
+    if kind == "zero queries":
+        q.zero_()
+    elif kind == "one zero query":
+        q[:, 2] = 0
+    else:
+        q[..., 4] = 0
+        put(c, "k", 123, {4: 0x7e}, 246)                  # 448 * 2^119 where every query is 0
     check_all(c, q, *run(c, q, "dense"))
 
 
