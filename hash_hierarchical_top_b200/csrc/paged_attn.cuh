@@ -239,6 +239,12 @@ __device__ __forceinline__ uint32_t row_of(const PageAttnArgs& a, const RowKeys&
   return ((uint32_t)page * (uint32_t)a.G + r.g) * (uint32_t)a.P + (uint32_t)slot;
 }
 
+// Two query channels under a scale of 0, which leaves nothing of finite ones (their products with
+// the keys might pass fp32's range); infinities and NaNs stay.
+__device__ __forceinline__ uint32_t without_finite(uint32_t w) {
+  return w & __vcmpeq2(w & 0x7f807f80u, 0x7f807f80u);
+}
+
 // Shared memory of one warp: NS stages of a K tile and a V tile, S rows each (16 bf16 or
 // 32 8-bit rows: 4 KB a tile). The 16-byte chunks of a row are XOR-swizzled by row % 8, so that
 // ldmatrix reads of 8 rows hit 8 distinct bank groups.
@@ -345,7 +351,9 @@ __device__ __forceinline__ void warp_fp32(const PageAttnArgs& a, const RowKeys& 
   float4 qf[NH];
 #pragma unroll
   for (int h = 0; h < NH; ++h) {
-    qf[h] = bf16x4_to_f4(*reinterpret_cast<const uint2*>(q + (size_t)min(h, n - 1) * kD + 4 * lane));
+    uint2 w = *reinterpret_cast<const uint2*>(q + (size_t)min(h, n - 1) * kD + 4 * lane);
+    if (a.scale_log2 == 0.f) w = make_uint2(without_finite(w.x), without_finite(w.y));
+    qf[h] = bf16x4_to_f4(w);
     o[h] = make_float4(0.f, 0.f, 0.f, 0.f);
     m[h] = -INFINITY;
     l[h] = 0.f;
@@ -554,7 +562,7 @@ __device__ __forceinline__ bool page_segment(const PageAttnArgs& a, const RowKey
   // A negative scale goes into the queries' signs, so that the largest product is the largest
   // logit: logit = hs * product in log2 units, hs > 0.
   if constexpr (!kSoon) load_q();
-  float hs = fmaxf(fabsf(a.scale_log2), 1.17549435e-38f);
+  float hs = a.scale_log2 != 0.f ? fabsf(a.scale_log2) : 1.f;
   // 8-bit: the smallest exponent byte of this lane's values, less 1 (a missing row's 0 becomes the
   // largest), and the largest one of its keys (255: queries that f16 does not hold).
   uint32_t x_low = 0xffffffffu, x_key = 0u;
@@ -564,6 +572,13 @@ __device__ __forceinline__ bool page_segment(const PageAttnArgs& a, const RowKey
     for (int i = 0; i < 8; ++i) {
       qa[i][0] = hv ? qa[i][0] ^ sign : 0u;
       qa[i][1] = hv ? qa[i][1] ^ sign : 0u;
+    }
+    if (a.scale_log2 == 0.f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        qa[i][0] = without_finite(qa[i][0]);
+        qa[i][1] = without_finite(qa[i][1]);
+      }
     }
     if constexpr (K8) {
       // Bits of the largest channel (of the column) and of the smallest that is not 0 (of the lane,

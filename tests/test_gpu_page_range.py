@@ -218,3 +218,26 @@ def test_nan_and_infinite_queries_act_on_their_heads_only(path, n):
         o, l, to, tl = ref_rows(q[0, keep], c.rows("k", 0, 0, pos), c.rows("v", 0, 0, pos), SCALE)
         check(out[keep], o, to, "rest")
         check(lse[keep], l, tl, "rest lse")
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("n", [600, 9001])
+@pytest.mark.parametrize("qs,ks,scale", [(60, 58, 0.0), (60, 58, -0.0), (100, 24, 0.0), (60, 58, 2.0 ** -128),
+                                         (60, 58, -2.0 ** -127), (20, -19, 1.0)])
+def test_scales_of_zero_and_below_the_normal_range(qs, ks, scale, n, kv8):
+    """A scale of 0 is the plain mean, however large the products are; one below 2^-126 is taken as it is."""
+    build.build()
+    c = Paged([n], 1, 4, 32, kv8, seed=800, scale=2.0 ** ks)
+    q = (c.queries(1).float() * 2.0 ** qs).bfloat16()
+    out, lse = run(c, q, "dense", scale)
+    check_all(c, q, out, lse, scale)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_a_scale_of_zero_keeps_infinite_and_nan_queries(kv8):
+    build.build()
+    c = Paged([300], 1, 4, 32, kv8, seed=801)
+    q = c.queries(1)
+    q[0, 1, 5], q[0, 2, 6] = math.nan, -math.inf
+    out, lse = run(c, q, "dense", 0.0)
+    assert torch.isnan(out[1:3]).all() and torch.isfinite(out[[0, 3]]).all()
