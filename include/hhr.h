@@ -352,6 +352,8 @@ size_t hhr_paged_attn_workspace_bytes(const hhr_dims* dims);
  *   k_new, v_new : NULL, or bf16 [B][G][d]: the rows of position seq_len[b] - 1, written into
  *                  the cache (quantised as hhr_append_kv8 does, when it holds 8 bits) by this
  *                  call before they are attended to. A sequence of length 0 writes nothing.
+ *                  Nothing but these rows is written: where block means, page summaries or codes
+ *                  of the cache are in use, append with hhr_append_kv8 or hhr_encode_keys instead.
  *   dims.select_per_head must be 0. seq_len[b] beyond max_pages_per_seq * P is clipped to it
  *   and flagged (its new row, which has no page, is not written); a key whose page-table entry is out of range is skipped and flagged. */
 int hhr_paged_attn(const hhr_dims* dims, const uint16_t* q, const uint16_t* k_new,

@@ -154,3 +154,74 @@ def test_unsupported_sizes_are_refused():
                  lambda: BlockStep(hhr.make_dims(1, 8, 2, 16, 4, 4), 1, 0, "cuda")):
         with pytest.raises(ValueError):
             make()
+
+
+@pytest.mark.parametrize("own_stream", [False, True])
+def test_a_dense_step_keeps_the_block_means(own_stream):
+    """Tokens appended by dense steps to a cache with block means: the means are those of the rows, so
+    that a block-sparse step can follow; rows and outputs are those of a cache without means."""
+    build.build()
+    B, G, gs, P, maxp = 3, 2, 4, 8, 9
+    lens = [13, 0, 40]
+    d = hhr.make_dims(B, G * gs, G, P, maxp, B * maxp)
+    gen = torch.Generator(device="cuda").manual_seed(23)
+    bf = lambda *s: torch.randn(*s, generator=gen, device="cuda").bfloat16()
+    pt = torch.randperm(B * maxp, generator=gen, device="cuda").int().reshape(B, maxp)
+    with_means, plain = KV8Cache(d, "cuda", block_means=True), KV8Cache(d, "cuda")
+    prompt = bf(B, max(lens), 2 * G, D)
+    for c in (with_means, plain):
+        c.append(prompt[:, :, :G], prompt[:, :, G:], i32([0] * B), i32(lens), pt)
+    steps = DenseStep(d, "cuda"), DenseStep(d, "cuda")
+    stream = torch.cuda.Stream() if own_stream else None
+    block = BlockStep(d, 1, 3, "cuda")
+    for step in range(1, 19):
+        # Sequence 1 stays empty for a while: nothing of it is written.
+        n = [lens[0] + step, max(0, step - 5), lens[2] + step]
+        seq_len, q, kn, vn = i32(n), bf(B, G * gs, D), bf(B, G, D), bf(B, G, D)
+        torch.cuda.synchronize()
+        a = steps[0].attend(q, with_means, pt, seq_len, kn, vn, stream=stream)
+        torch.cuda.synchronize()
+        b = steps[1].attend(q, plain, pt, seq_len, kn, vn)
+        status_ok()
+        assert torch.equal(a, b) and torch.equal(steps[0].lse, steps[1].lse)
+        for x, y in ((with_means.k, plain.k), (with_means.v, plain.v)):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+        assert torch.equal(with_means.k_exp, plain.k_exp) and torch.equal(with_means.v_exp, plain.v_exp)
+    for b in range(B):
+        for g in range(G):
+            k, _ = rows_of(with_means, pt, b, g, torch.arange(n[b], device="cuda"), P)
+            for p in range(-(-n[b] // P)):
+                x = k[p * P:(p + 1) * P]
+                err = (with_means.block_mean[int(pt[b, p]), g].double() - x.mean(0)).abs()
+                # At most P + 16 roundings of fp32 sums, and the division.
+                assert (err <= (P + 18) * 2.0 ** -24 * x.abs().mean(0)).all(), (b, g, p)
+    block.step(q[:, None], with_means, pt, seq_len)
+    status_ok()
+    assert block.count[:, 0, 0].tolist() == [min(3, -(-x // P)) for x in n]
+
+
+def test_a_captured_dense_step_keeps_the_block_means():
+    build.build()
+    B, G, P, maxp = 2, 1, 4, 6
+    d = hhr.make_dims(B, 2, G, P, maxp, B * maxp)
+    pt = torch.arange(B * maxp, dtype=torch.int32, device="cuda").reshape(B, maxp)
+    cache, step = KV8Cache(d, "cuda", block_means=True), DenseStep(d, "cuda")
+    q, kn, vn = (torch.randn(B, h, D, device="cuda").bfloat16() for h in (2, 1, 1))
+    seq_len = i32([0, 0])
+    step.attend(q, cache, pt, seq_len, kn, vn)               # outside a capture first: writes nothing
+    torch.cuda.synchronize()
+    assert not cache.k_exp.any() and not cache.block_mean.any()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.attend(q, cache, pt, seq_len, kn, vn)
+    for n in range(1, 11):
+        seq_len.copy_(i32([n, max(0, n - 4)]))
+        kn.normal_()
+        graph.replay()
+        status_ok()
+    for b, n in ((0, 10), (1, 6)):
+        k, _ = rows_of(cache, pt, b, 0, torch.arange(n, device="cuda"), P)
+        for p in range(-(-n // P)):
+            x = k[p * P:(p + 1) * P]
+            err = (cache.block_mean[int(pt[b, p]), 0].double() - x.mean(0)).abs()
+            assert (err <= (P + 18) * 2.0 ** -24 * x.abs().mean(0)).all()
