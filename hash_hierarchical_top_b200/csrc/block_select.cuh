@@ -434,16 +434,19 @@ __global__ void __launch_bounds__(NT) block_topm_kernel(BlockSelectArgs a) {
     asq += nq[w];
     nmax = fmaxf(nmax, nm[w]);
   }
-  int k = min(a.m_pages, live_n);  // forced ones are at most m_pages
+  int k = min(a.m_pages, live_n);  // forced ones are at most m_pages, and all live
   const bool sound = asq > 1e-30f && asq < 1e36f && nmax > 1e-30f && nmax < 1e36f;
   auto value = [](uint32_t key) {
     return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
   };
   bool done = n == 0;
-  if (!done && sound && k == live_n) {
+  // Nothing but the forced blocks is kept.
+  const bool none_free = min(n, a.sink + a.local) == min(n, a.m_pages);
+  if (!done && (none_free || (sound && k == live_n))) {
     for (int w = warp; w < words; w += NW) {
       const int i = 32 * w + lane;
-      const unsigned m = __ballot_sync(kFull, i < n && bs_keys[i] != 0u);
+      const uint32_t kk = i < n ? bs_keys[i] : 0u;
+      const unsigned m = __ballot_sync(kFull, none_free ? kk == 0xffffffffu : kk != 0u);
       if (lane == 0) bits[w] = m;
     }
     __syncthreads();
@@ -483,60 +486,59 @@ __global__ void __launch_bounds__(NT) block_topm_kernel(BlockSelectArgs a) {
     }
     __syncthreads();
     const int bin = found[0];
-    if (bin < kBins - 1) {  // else more are forced than are kept, which the caller rules out
-      // The bin's values, and an allowance for the rounding of bin_of, widened by 2E.
-      const float e2 = 2.f * kBsErr * sqrtf(asq) * sqrtf(nmax) + 4e-6f * (fabsf(lo) + fabsf(value(kmax)));
-      const float low = lo + bin * width - e2, hi = lo + (bin + 1) * width + e2;
-      int sure = 0;
-      for (int w0 = warp; w0 < words; w0 += LU * NW) {
-        uint32_t kk[LU];
+    // The cut lies below the forced blocks' bin: more than those are kept.
+    // The bin's values, and an allowance for the rounding of bin_of, widened by 2E.
+    const float e2 = 2.f * kBsErr * sqrtf(asq) * sqrtf(nmax) + 4e-6f * (fabsf(lo) + fabsf(value(kmax)));
+    const float low = lo + bin * width - e2, hi = lo + (bin + 1) * width + e2;
+    int sure = 0;
+    for (int w0 = warp; w0 < words; w0 += LU * NW) {
+      uint32_t kk[LU];
 #pragma unroll
-        for (int j = 0; j < LU; ++j) {
-          const int i = 32 * (w0 + j * NW) + lane;
-          kk[j] = i < n ? bs_keys[i] : 0u;
-        }
-        unsigned band_of = 0u;  // bit j: this lane's j-th block is collected
-        uint32_t mine = 0u;     // lane j < LU: the j-th word
-#pragma unroll
-        for (int j = 0; j < LU; ++j) {
-          const float s = value(kk[j]);
-          const bool over = kk[j] == 0xffffffffu || (kk[j] != 0u && s > hi);
-          const unsigned m = __ballot_sync(kFull, over);
-          if (lane == j) mine = m;
-          if (kk[j] != 0u && !over && s >= low) band_of |= 1u << j;
-        }
-        if (lane < LU && w0 + lane * NW < words) bits[w0 + lane * NW] = mine;
-        sure += __popc(mine);
-        for (; band_of != 0u; band_of &= band_of - 1u) {
-          const int at = atomicAdd(&found[1], 1);  // in any order: the ranks do not depend on it
-          if (at < kPickMax) cand_at[at] = 32 * (w0 + (__ffs(band_of) - 1) * NW) + lane;
-        }
+      for (int j = 0; j < LU; ++j) {
+        const int i = 32 * (w0 + j * NW) + lane;
+        kk[j] = i < n ? bs_keys[i] : 0u;
       }
-      sure = __reduce_add_sync(kFull, sure);
-      if (lane == 0) atomicAdd(&found[2], sure);
-      __syncthreads();
-      const int band = found[1], want = k - found[2];
-      if (band <= kPickMax) {
-        if (band != want) {
-          double q[4];
-          bs_query_sum(qrow + 4 * lane, gs, q);
-          for (int c = warp; c < band; c += NW) {
-            const float s = bs_exact(a, b, g, cand_at[c], q, lane);
-            if (lane == 0) cand_key[c] = f2key(s);
-          }
-          __syncthreads();
-        }
-        if (tid < band) {
-          const int i = cand_at[tid];
-          int rank = 0;
-          if (band != want)
-            for (int j = 0; j < band; ++j)
-              rank += cand_key[j] > cand_key[tid] || (cand_key[j] == cand_key[tid] && cand_at[j] < i);
-          if (rank < want) atomicOr(&bits[i >> 5], 1u << (i & 31));
+      unsigned band_of = 0u;  // bit j: this lane's j-th block is collected
+      uint32_t mine = 0u;     // lane j < LU: the j-th word
+#pragma unroll
+      for (int j = 0; j < LU; ++j) {
+        const float s = value(kk[j]);
+        const bool over = kk[j] == 0xffffffffu || (kk[j] != 0u && s > hi);
+        const unsigned m = __ballot_sync(kFull, over);
+        if (lane == j) mine = m;
+        if (kk[j] != 0u && !over && s >= low) band_of |= 1u << j;
+      }
+      if (lane < LU && w0 + lane * NW < words) bits[w0 + lane * NW] = mine;
+      sure += __popc(mine);
+      for (; band_of != 0u; band_of &= band_of - 1u) {
+        const int at = atomicAdd(&found[1], 1);  // in any order: the ranks do not depend on it
+        if (at < kPickMax) cand_at[at] = 32 * (w0 + (__ffs(band_of) - 1) * NW) + lane;
+      }
+    }
+    sure = __reduce_add_sync(kFull, sure);
+    if (lane == 0) atomicAdd(&found[2], sure);
+    __syncthreads();
+    const int band = found[1], want = k - found[2];
+    if (band <= kPickMax) {
+      if (band != want) {
+        double q[4];
+        bs_query_sum(qrow + 4 * lane, gs, q);
+        for (int c = warp; c < band; c += NW) {
+          const float s = bs_exact(a, b, g, cand_at[c], q, lane);
+          if (lane == 0) cand_key[c] = f2key(s);
         }
         __syncthreads();
-        done = true;
       }
+      if (tid < band) {
+        const int i = cand_at[tid];
+        int rank = 0;
+        if (band != want)
+          for (int j = 0; j < band; ++j)
+            rank += cand_key[j] > cand_key[tid] || (cand_key[j] == cand_key[tid] && cand_at[j] < i);
+        if (rank < want) atomicOr(&bits[i >> 5], 1u << (i & 31));
+      }
+      __syncthreads();
+      done = true;
     }
   }
   if (!done) {

@@ -270,3 +270,43 @@ def test_append_select_attend(T):
                 h = slice(g * gs, (g + 1) * gs)
                 check_rows(out[b, t, h], lse[b, t, h], q[b, t, h], c.rows("k", b, g, pos),
                            c.rows("v", b, g, pos), 1 / math.sqrt(D), f"{b} {g} {t}")
+
+
+@pytest.mark.parametrize("kind", ["ordinary", "huge", "nan"])
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("sink,local", [(1, 0), (0, 1), (1, 2), (3, 1), (0, 64)])
+def test_every_kept_block_is_forced(sink, local, T, kind):
+    """As many blocks kept as are forced, and one more (the best of the rest): with scores that fp32
+    holds, and with ones that it does not."""
+    build.build()
+    P, G, lens = 16, 2, [3000 * 16, 37, 65 * 16 - 1]
+    gen = torch.Generator(device="cuda").manual_seed(13)
+    pages = [-(-n // P) for n in lens]
+    maxp, n_phys = max(pages), sum(pages)
+    means = torch.randn(n_phys, G, D, generator=gen, device="cuda")
+    if kind == "huge":
+        means *= 1e37
+    elif kind == "nan":
+        means[::7, :, 3] = math.nan
+    pt = torch.full((3, maxp), -1, dtype=torch.int32, device="cuda")
+    order, at = torch.randperm(n_phys, generator=gen, device="cuda").int(), 0
+    for b, n in enumerate(pages):
+        pt[b, :n] = order[at:at + n]
+        at += n
+    d = hhr.make_dims(3, 8, G, P, maxp, n_phys)
+    q = torch.randn(3, T, 8, D, generator=gen, device="cuda").bfloat16()
+    seq_len = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    for m in (sink + local, sink + local + 1):
+        blocks, count = select(d, q, seq_len, None, pt, means, m, hhr.make_opts(sink, local))
+        status_ok()
+        for b, n in enumerate(pages):
+            forced = set(range(min(sink, n))) | set(range(max(0, n - local), n))
+            for g in range(G):
+                mean = means[pt[b, :n].long(), g].double()
+                for t in range(T):
+                    s = (mean @ q[b, t, 4 * g:4 * g + 4].double().sum(0)).float().tolist()
+                    # (Forced blocks come before any score: huge ones are +inf in fp32.)
+                    rest = sorted((-x, p) for p, x in enumerate(s) if x > -math.inf and p not in forced)
+                    want = sorted(list(forced) + [p for _, p in rest[:max(0, m - len(forced))]])
+                    assert blocks[b, t, g, :int(count[b, t, g])].tolist() == want
+                    assert (blocks[b, t, g, len(want):] == -1).all()
