@@ -35,11 +35,26 @@ def _fresh(target, srcs):
                                           for s in srcs)
 
 
+def binding_tag() -> str:
+    """What _binding.so is built against: it uses torch's C++ types and Python's C API, which hold
+    for one release each."""
+    import torch
+    return f"hhr binding for torch {torch.__version__}, {sys.implementation.cache_tag}"
+
+
+def binding_matches(path: str = BINDING) -> bool:
+    """Whether the module at `path` was built against the installed torch and Python (the tag is one
+    of its strings, so that it need not be loaded to be asked)."""
+    with open(path, "rb") as f:
+        return binding_tag().encode() + b"\0" in f.read()
+
+
 def build_binding(force: bool = False):
-    """Start compiling _binding.so (against the installed torch's headers) if it is missing or
-    older than its sources; returns the process, or None."""
+    """Start compiling _binding.so (against the installed torch's headers) if it is missing, older
+    than its sources or built against another torch or Python; returns the process, or None."""
     src = os.path.join(CSRC, "binding.cpp")
-    if not force and _fresh(BINDING, [src, os.path.join(ROOT, "include", "hhr.h")]):
+    if (not force and _fresh(BINDING, [src, os.path.join(ROOT, "include", "hhr.h")])
+            and binding_matches()):
         return None
     import torch
     from torch.utils.cpp_extension import CUDA_HOME, include_paths
@@ -48,14 +63,15 @@ def build_binding(force: bool = False):
                              os.path.join(CUDA_HOME or "/usr/local/cuda", "include")]
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DHHR_BUILT_FOR="{binding_tag()}"',
            *(f"-I{i}" for i in inc), "-o", BINDING + ".tmp", src, f"-L{libs}",
            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     return subprocess.Popen(cmd)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libhhr.so and _binding.so where they are missing or older than a source; return
-    the library's path."""
+    """Compile libhhr.so and _binding.so where they are missing or out of date; return the
+    library's path."""
     binding = build_binding(force)
     try:
         return _build_lib(force, verbose)

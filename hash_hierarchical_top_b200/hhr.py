@@ -313,13 +313,18 @@ _binding = None
 
 
 def _native():
-    """The loaded _binding.so, bound to the loaded library (raises if it has not been built)."""
+    """The loaded _binding.so, bound to the loaded library (raises if it has not been built, or was
+    built against another torch or Python)."""
     global _binding
     if _binding is None:
         path = os.path.join(HERE, "_binding.so")
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing: build it with "
                                "`python -m hash_hierarchical_top_b200.build`")
+        from . import build  # (not above: it is also run as a module)
+        if not build.binding_matches(path):
+            raise RuntimeError(f"{path} was not built as the {build.binding_tag()}: build it anew "
+                               "with `python -m hash_hierarchical_top_b200.build`")
         loader = importlib.machinery.ExtensionFileLoader("_binding", path)
         spec = importlib.util.spec_from_loader("_binding", loader)
         module = importlib.util.module_from_spec(spec)

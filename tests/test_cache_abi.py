@@ -204,3 +204,18 @@ def test_binding_follows_a_reloaded_library(L, monkeypatch):
     assert hhr.lib()._bound is module
     monkeypatch.setattr(hhr, "_lib", None)
     assert hhr._native() is module and hhr.lib()._bound is module
+
+
+def test_binding_of_another_torch_is_rebuilt_and_refused(L, monkeypatch):
+    """The module holds what it was built against; with another torch it is neither kept nor loaded."""
+    assert build.binding_matches() and build.build_binding() is None
+    assert hhr._native().built_for == build.binding_tag()
+    started = []
+    monkeypatch.setattr(build.subprocess, "Popen", lambda cmd, **kw: started.append(cmd))
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".1")
+    assert not build.binding_matches()
+    build.build_binding()
+    assert len(started) == 1 and any(build.binding_tag() in x for x in started[0])
+    monkeypatch.setattr(hhr, "_binding", None)
+    with pytest.raises(RuntimeError, match="build it anew"):
+        hhr._native()
