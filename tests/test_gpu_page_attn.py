@@ -519,3 +519,68 @@ def test_cache_rows_past_2_to_31_bytes():
     out, lse = dense(c, q)
     status_ok()
     check_dense(c, q, out, lse)
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("lens,G,gs,P,T,m,causal", [
+    ([40000], 1, 3, 64, 1, 300, False),
+    ([30000, 25000], 2, 5, 128, 1, 400, False),
+    ([20000], 1, 8, 32, 3, 1000, True),
+    ([16000, 300], 2, 4, 16, 2, 1024, True),
+    ([9000], 1, 6, 17, 2, 600, False),
+    ([12000, 0, 12000], 1, 1, 100, 1, 90, False),
+])
+def test_long_lists_of_few_rows(lens, G, gs, P, T, m, causal, kv8, per_head):
+    """Lists of more than 8192 keys whose rows do not fill the GPU: every row is split evenly over many
+    CTAs by its capacity, whatever its count (the whole list, none, one block, a third)."""
+    build.build()
+    c = Paged(lens, G, gs, P, kv8, seed=131 + P)
+    c.d.select_per_head = int(per_head)
+    rows = G * gs if per_head else G
+    q = c.queries(len(lens), T)
+    q_pos = (torch.linspace(max(lens) // 3, max(lens) + 3, T, device="cuda").int().expand(len(lens), T)
+             .contiguous() if causal else None)
+    gen = torch.Generator(device="cuda").manual_seed(7 * P + T)
+    pages = torch.tensor([max(1, -(-n // P)) for n in lens], device="cuda")
+    blocks = (torch.rand(len(lens), T, rows, m, generator=gen, device="cuda") *
+              pages[:, None, None, None]).int()
+    full = [m, 0, 1, m // 3, m]
+    count = torch.tensor([full[i % 5] if lens[i // (T * rows)] else 0 for i in range(len(lens) * T * rows)],
+                         dtype=torch.int32, device="cuda").reshape(len(lens), T, rows)
+    for dtype in (torch.float32, torch.bfloat16):
+        out, lse = sparse(c, q, blocks, count, q_pos, dtype)
+        status_ok()
+        check_sparse(c, q, blocks, count, q_pos, out, lse)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("B,n", [(1, 517), (1, 8000), (1, 131072), (450, 16384)])
+@pytest.mark.parametrize("gs", [4, 8])
+def test_outputs_are_as_exact_as_fp32_sums(gs, B, n, kv8):
+    """The error over all outputs, relative to their size, where errors are independent of one another.
+    A weight is off by at most 2^-22 by each of its logit (of size 4), exp2 and its operand parts, by
+    2^-22 or less rms in all; over the 190 or more keys that carry a row of 517 an output of 0.25 and
+    values of size 1 makes 0.3 of that; a step's and the running fp32 sums add about 2^-24 each. So 2^-22
+    is twice what is to be expected. Weights in two bf16 parts (2^-18 each), or sums kept in the matrix
+    units' truncating accumulator (a bias that grows with the steps of a warp: 512 where the 450
+    sequences, which share their pages, leave every CTA a whole row), are over it."""
+    build.build()
+    c = Paged([n], 1, gs, 32, kv8, seed=97)
+    c.d.batch = B
+    c.pt, c.seq_len = c.pt.expand(B, -1).contiguous(), c.seq_len.expand(B).contiguous()
+    q = c.queries(B)
+    out, lse = dense(c, q)
+    status_ok()
+    pos = torch.arange(n, device="cuda")
+    k, v = c.rows("k", 0, 0, pos), c.rows("v", 0, 0, pos)
+    err = size = 0.0
+    for b in range(0, B, 60):
+        s = SCALE * (q[b].double() @ k.T)
+        ref = torch.softmax(s, -1) @ v
+        err += float((out[b].double() - ref).square().sum())
+        size += float(ref.square().sum())
+        assert float((lse[b].double() - torch.logsumexp(s, -1)).abs().max()) < 1e-5
+    err = math.sqrt(err / size)
+    print(f"relative error {err:.2e}")
+    assert err < 2.0 ** -22, err
