@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kReadThreads) read_kv8_kernel(ReadArgs a) {
       if (lane == 0) flag_status(kStatusBadToken);
       continue;
     }
-    // t / P: t < 2^23 and P <= 256, so the error of the product is below 1 / P.
+    // t / P: t < 2^23 and P <= 256, so the product is too large by less than 2^-9 < 1 / P.
     const int lp = a.P == 1 ? (int)t : (int)__umulhi((uint32_t)t, a.p_mul);
     const int phys = a.page_table[(size_t)b * a.maxp + lp];
     if (phys < 0 || phys >= a.n_phys) {

@@ -51,23 +51,11 @@
 
 namespace hhr {
 
-#ifndef HHR_PA_WARPS
-#define HHR_PA_WARPS 4
-#endif
-#ifndef HHR_PA_CTAS
-#define HHR_PA_CTAS 3
-#endif
-#ifndef HHR_PA_UNIT
-#define HHR_PA_UNIT 128
-#endif
-#ifndef HHR_PA_STAGES
-#define HHR_PA_STAGES 2
-#endif
-constexpr int kPaStages = HHR_PA_STAGES;
-constexpr int kPaWarps = HHR_PA_WARPS;
+constexpr int kPaStages = 2;
+constexpr int kPaWarps = 4;
 constexpr int kPaThreads = kPaWarps * 32;
-constexpr int kPaCtasPerSm = HHR_PA_CTAS;
-constexpr int kUnitKeys = HHR_PA_UNIT;
+constexpr int kPaCtasPerSm = 3;
+constexpr int kUnitKeys = 128;
 
 struct PageAttnArgs {
   const uint16_t* q;      // [B][T][Hq][d]
@@ -94,7 +82,8 @@ struct PageAttnArgs {
   uint32_t n_rows;             // n_phys G P
 };
 
-// j / P for 0 <= j < 2^24, P <= 256: the error of j p_mul / 2^32 is below j P / 2^32 < 1 / P.
+// j / P for 0 <= j < 2^24, P <= 256: p_mul exceeds 2^32 / P by less than 1, so that j p_mul / 2^32 is
+// too large by less than j / 2^32 < 2^-8 <= 1 / P.
 __device__ __forceinline__ int page_of(const PageAttnArgs& a, int j) {
   return a.P == 1 ? j : (int)__umulhi((uint32_t)j, a.p_mul);
 }
@@ -821,13 +810,7 @@ static_assert(kMaxGroup * (kD + 2) * 4 <= kPaStages * kPaStage, "a warp's state 
 // outputs (at most kMaxGroup d, rounded up per rank), then per rank and head (maximum, sum).
 // Three stages at two CTAs per SM are no faster (8 sequences x 64 pages: 14.3 us either way; 48
 // queries x 16 pages: 24.7 us against 18.4 us).
-#ifndef HHR_PC_STAGES
-#define HHR_PC_STAGES 2
-#endif
-#ifndef HHR_PC_CTAS
-#define HHR_PC_CTAS 3
-#endif
-constexpr int kPcStages = HHR_PC_STAGES, kPcCtasPerSm = HHR_PC_CTAS, kPaMaxCluster = 8;
+constexpr int kPcStages = 2, kPcCtasPerSm = 3, kPaMaxCluster = 8;
 constexpr int kPcShares = kMaxGroup * kD + kPaMaxCluster;                          // floats
 constexpr int kPcInbox = kPcShares + 2 * kPaMaxCluster * kMaxGroup;
 inline size_t page_cluster_smem() {
