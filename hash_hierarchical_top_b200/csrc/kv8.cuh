@@ -109,8 +109,8 @@ constexpr int kAppendRows = kAppendThreads / 16;  // rows per pass: 16 lanes eac
 constexpr int kAppendUnroll = 2;
 
 // One CTA per (touched page, KV group, sequence). 16 lanes quantise a row, 8 channels a lane.
-// A prefill is bound by instructions as much as by its bytes: 178K rows of K and V take 27 us (137
-// MB, 5.1 TB/s, 77% of the copy rate); 41 us with scalar maxima, one tensor after the other and
+// A prefill is bound by instructions as much as by its bytes: 178K rows of K and V take 27.7 us (137
+// MB, 4.95 TB/s, 75% of the copy rate); 41 us with scalar maxima, one tensor after the other and
 // CTAs of 256 threads. A token per sequence takes 3.3 us, all of it latency.
 // With block_mean, the K rows that the page held before are read too, and the mean is taken
 // over the values that the cache stands for.

@@ -26,9 +26,10 @@
 // P is used in parts (bf16: three, f16: two), so that the fp32 output is not limited by the matrix
 // operands' type: 2e-7 to 5e-7 off the 64-bit result at 517 to 128K keys.
 //
-// Measured (B200, calls in a row): 8 x 128K keys x 8 KV heads in bf16 620-630 us, 6.8-6.9 TB/s of K
-// and V (the measured copy rate is 6.55); 16 ragged sequences of 8K to 128K keys in 8 bits 388-408
-// us, 6.2-6.5 TB/s; 1 x 32K keys 30.3 us, of which the stream takes 21; 1 x 517 keys 5.7 us.
+// Measured (B200, calls in a row): 8 x 128K keys x 8 KV heads in bf16 635-640 us, 6.7 TB/s of K and V
+// (the measured copy rate is 6.55); 16 ragged sequences of 8K to 128K keys in 8 bits 409-414 us, 6.1
+// TB/s; 1 x 32K keys 30.6 us, of which the stream takes 21; 1 x 517 keys 5.7 us, where the page table
+// is no wider than 4096 keys.
 //
 // 8-bit cache: e4m3 numbers become f16 exactly. Q is scaled by a power of two per head so that
 // its largest channel is in [2^14, 2^15): a bf16 query is then exact in f16 where its channels lie
@@ -37,7 +38,9 @@
 // out of f16's subnormal range: with value exponents within kPaSpread of one another, a weight is
 // off by 2^-22 of itself or 2^-25 of the largest one. A warp that meets anything else (value
 // exponents further apart, keys or queries that would leave fp32 on the way to an ordinary logit) has
-// its keys taken again in plain fp32 (warp_fp32), at about a tenth of the rate.
+// its keys, and in even shares its CTA's, taken again in plain fp32 (warp_fp32). 4 x 64K keys 93 us,
+// with one such row in every page 651 us, with one row of zeros in every page, which only has to be
+// looked at, 134 us.
 //
 // Split of the work: the rows' keys, in units of kUnitKeys, are laid end to end and divided
 // evenly over the CTAs (three per SM), whatever the lengths; a CTA's share covers the end of one

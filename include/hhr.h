@@ -330,17 +330,25 @@ int hhr_read_kv8(const hhr_dims* dims, const uint8_t* k, const uint8_t* v, const
 /* ---- Attention over whole pages ---------------------------------------------------------
  * Two calls that attend to every key of the pages they are given, from a bf16 cache (k_exp and
  * v_exp NULL) or an 8-bit one. out[..][h] = sum_j softmax_j(scale * q_h . k_j) v_j, with
- * statistics and sums in fp32; a row with no key gives zeros. Keys outside the mask are never
+ * products, statistics and sums in fp32: q . k beyond its range is infinite, and so is a value times
+ * the sum of the weights (of which the largest is 1, before they are divided by that sum); a weight
+ * below 2^-126 is 0. A row with no key gives zeros. Keys outside the mask are never
  * read into the sums, whatever the cache holds there; keys whose logit is -inf have weight 0; a
  * NaN key or a logit of +inf makes its head's output NaN, an infinite or NaN value its channel.
+ * An 8-bit cache may hold any exponents that hhr_append_kv8 writes. Where the value rows of a
+ * sequence (rows of zeros aside) span more than 14 binades, keys pass 2^104, or the channels of a
+ * query that are not 0 span more than 31 binades, the keys near them take up to seven times as long.
  *   out      : [B][T][Hq][d], f32, or bf16 with out_bf16 = 1 (rounded once)
  *   lse      : NULL, or f32 [B][T][Hq]: log sum_j exp(scale * q_h . k_j), with which outputs
  *              over disjoint key sets can be joined; -inf for a row with no key
  *   workspace: at least the call's *_workspace_bytes (0 on invalid input), on the device that
  *              the call runs on. Its contents need not be kept or cleared, but calls that can
  *              overlap on the GPU need one each.
- * The keys of all rows are divided evenly over the GPU, whatever the sequences' lengths; rows
- * that are split are joined in a fixed order, so that equal inputs give equal bits. The first
+ * The work is divided evenly over the GPU: dense rows by their lengths, whatever these are; lists
+ * by their capacity m_max * P, so that a count well below m_max leaves part of the GPU idle. Rows of
+ * a few thousand keys at most (by max_pages_per_seq * P, or m_max * P) take one kernel, others a
+ * second one that joins their parts. Rows that are split are joined in a fixed order, so that equal
+ * inputs give equal bits. The first
  * call of a kind on a device loads its kernel and raises its shared-memory limit: make it before
  * capturing the call into a CUDA graph (this holds for hhr_block_select too). */
 
@@ -355,7 +363,8 @@ size_t hhr_paged_attn_workspace_bytes(const hhr_dims* dims);
  *                  Nothing but these rows is written: where block means, page summaries or codes
  *                  of the cache are in use, append with hhr_append_kv8 or hhr_encode_keys instead.
  *   dims.select_per_head must be 0. seq_len[b] beyond max_pages_per_seq * P is clipped to it
- *   and flagged (its new row, which has no page, is not written); a key whose page-table entry is out of range is skipped and flagged. */
+ *   and flagged (its new row, which has no page, is not written); a key whose page-table entry is
+ *   out of range is skipped and flagged. */
 int hhr_paged_attn(const hhr_dims* dims, const uint16_t* q, const uint16_t* k_new,
                    const uint16_t* v_new, void* k_cache, void* v_cache, uint8_t* k_exp,
                    uint8_t* v_exp, const int32_t* page_table, const int32_t* seq_len, float scale,
