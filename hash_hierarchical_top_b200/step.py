@@ -6,17 +6,32 @@ and outputs of one decode step and runs append-encode -> select -> sparse
 attention through the C ABI on one stream. ``KV8Cache`` is a layer's 8-bit K/V
 cache; ``DenseStep`` attends to every key of a cache (bf16 or 8-bit), and
 ``BlockStep`` selects blocks by their mean keys and attends to those, for one
-token or a chunk of queries per sequence. PyTorch only allocates memory here;
-every step of the path runs in the library's kernels.
+token or a chunk of queries per sequence. PyTorch only allocates memory here
+(and takes 1 from the lengths where block means are kept); every step of the path
+runs in the library's kernels.
 """
 from __future__ import annotations
 
-import contextlib
 import math
 
 import torch
 
 from . import hhr
+
+
+class _NewestRow:
+    """The newest row of every sequence, as the `start` and `n_new` of an append."""
+
+    def __init__(self, d: hhr.Dims, device):
+        self.start, self.one = (torch.ones(d.batch, dtype=torch.int32, device=device)
+                                for _ in range(2))
+
+    def position(self, seq_len, stream):
+        """seq_len - 1, on `stream` (a torch stream, a raw handle, or None for the current one)."""
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(getattr(stream, "cuda_stream", stream))
+        with torch.cuda.stream(stream):
+            return torch.sub(seq_len.reshape(-1)[:len(self.start)], 1, out=self.start)
 
 
 class LayerCache:
@@ -132,15 +147,6 @@ def _cache_args(cache):
     return k, v, None, None
 
 
-def _stream_of(stream):
-    """A context in which torch works on `stream` (None: the current one; a raw handle is taken)."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream))
-    return torch.cuda.stream(stream)
-
-
 class DenseStep:
     """Workspace and outputs of dense decode attention: one new token per sequence over every key
     of its cache."""
@@ -153,27 +159,24 @@ class DenseStep:
         self.ws = torch.empty(n, dtype=torch.uint8, device=device)
         self.out = torch.empty(d.batch, d.n_q_heads, d.head_dim, dtype=out_dtype, device=device)
         self.lse = torch.empty(d.batch, d.n_q_heads, dtype=torch.float32, device=device)
-        # Position and count of the row that a step appends to a cache with block means.
-        self.newest, self.one = (torch.ones(d.batch, dtype=torch.int32, device=device)
-                                 for _ in range(2))
+        self.newest = _NewestRow(d, device)
 
     def attend(self, q, cache, page_table, seq_len, k_new=None, v_new=None, scale=None,
                stream=None):
         """cache: a KV8Cache, or (k_cache, v_cache) in bf16. k_new, v_new [B][G][d]: the rows of
-        position seq_len - 1, written by the same call; into a KV8Cache with block means by an
-        append before it, which keeps the means. Of a bf16 cache only the rows are written: its
-        page summaries, codes and block means (LayerCache) are the encoder's."""
+        position seq_len - 1, written by the same call. A KV8Cache with block means has them brought
+        up to date by an append of these rows behind it. Of a bf16 cache only the rows are written:
+        its page summaries, codes and block means (LayerCache) are the encoder's."""
         if scale is None:
             scale = 1.0 / math.sqrt(self.d.head_dim)
         k, v, k_exp, v_exp = _cache_args(cache)
-        if (isinstance(cache, KV8Cache) and cache.block_mean is not None and k_new is not None
-                and v_new is not None):
-            with _stream_of(stream):
-                torch.sub(seq_len, 1, out=self.newest)
-            cache.append(k_new, v_new, self.newest, self.one, page_table, stream)
-            k_new = v_new = None
         hhr.hhr_paged_attn(self.d, q, k_new, v_new, k, v, k_exp, v_exp, page_table, seq_len, scale,
                            self.out, self.ws, self.lse, stream)
+        if k_new is not None and isinstance(cache, KV8Cache) and cache.block_mean is not None:
+            k_new, v_new = (x.reshape(-1, 1, self.d.n_kv_heads, self.d.head_dim)[:self.d.batch]
+                            for x in (k_new, v_new))
+            cache.append(k_new, v_new, self.newest.position(seq_len, stream), self.newest.one,
+                         page_table, stream)
         return self.out
 
 

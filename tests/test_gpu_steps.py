@@ -225,3 +225,27 @@ def test_a_captured_dense_step_keeps_the_block_means():
             x = k[p * P:(p + 1) * P]
             err = (cache.block_mean[int(pt[b, p]), 0].double() - x.mean(0)).abs()
             assert (err <= (P + 18) * 2.0 ** -24 * x.abs().mean(0)).all()
+
+
+def test_a_refused_dense_step_writes_nothing_and_buffers_may_be_larger():
+    """The checks come before the append that keeps the means; new rows and lengths in buffers of a larger
+    batch, and new rows as [B, G d], are taken as without means."""
+    build.build()
+    B, G, P, maxp = 2, 2, 4, 6
+    d = hhr.make_dims(B, 4, G, P, maxp, B * maxp)
+    pt = torch.arange(B * maxp, dtype=torch.int32, device="cuda").reshape(B, maxp)
+    cache, step = KV8Cache(d, "cuda", block_means=True), DenseStep(d, "cuda")
+    q, kn, vn = (torch.randn(4, h, D, device="cuda").bfloat16() for h in (4, 2, 2))
+    n = i32([5, 3, 9, 9])
+    for bad in (dict(q=q.float()), dict(seq_len=n.long()), dict(v_new=None), dict(k_new=kn.cpu())):
+        a = dict(q=q, cache=cache, page_table=pt, seq_len=n, k_new=kn, v_new=vn)
+        with pytest.raises((TypeError, ValueError, hhr.HHRError)):
+            step.attend(**{**a, **bad})
+    status_ok()
+    assert not cache.k_exp.any() and not cache.v_exp.any() and not cache.block_mean.any()
+    step.attend(q, cache, pt, n, kn, vn)
+    means = cache.block_mean.clone()
+    step.attend(q, cache, pt, n, kn.reshape(4, -1), vn.reshape(4, -1))
+    status_ok()
+    assert torch.equal(cache.block_mean, means) and means.any() and int((cache.k_exp != 0).sum()) == B * G
+    assert step.newest.start.tolist() == [4, 2]
