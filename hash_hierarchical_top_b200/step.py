@@ -65,7 +65,7 @@ class DecodeStep:
         self.count = torch.empty(d.batch, rows, dtype=torch.int32, device=device)
         self.m_max = hhr.hhr_kept_max(d, m_pages, keep_div)
         self.attention = attention and mode == hhr.HHR_MODE_HASH
-        self.fused_ws = None
+        self.fused_ws = self.newest = None  # made by the first fused_step that needs them
         if self.attention:
             aws = hhr.hhr_attn_workspace_bytes(d, top_k)
             self.attn_ws = torch.empty(aws, dtype=torch.uint8, device=device)
@@ -91,7 +91,8 @@ class DecodeStep:
 
     def fused_step(self, q, k_cache, v_cache, page_table, seq_len, R, W, cache: LayerCache,
                    k_new=None, v_new=None, scale=None, stream=None):
-        """One decode step through hhr_decode_step (the fused single-call path)."""
+        """One decode step through hhr_decode_step (the fused single-call path), which encodes the
+        newest row; the block means of a cache that has them are brought up to date behind it."""
         if self.fused_ws is None:
             n = hhr.hhr_decode_step_workspace_bytes(self.d, self.m_pages, self.keep_div,
                                                     self.top_k)
@@ -102,6 +103,11 @@ class DecodeStep:
                             cache.page_minmax, cache.codes, self.m_pages, self.keep_div,
                             self.top_k, scale, self.idx, self.count, self.out, self.fused_ws,
                             stream, self.opts)
+        if cache.block_mean is not None:
+            if self.newest is None:
+                self.newest = _NewestRow(self.d, self.idx.device)
+            hhr.hhr_encode_keys(self.d, k_cache, page_table, self.newest.position(seq_len, stream),
+                                self.newest.one, 1, None, None, None, None, cache.block_mean, stream)
         return self.out
 
     def step(self, q, k_cache, v_cache, page_table, seq_len, R, W, cache: LayerCache,

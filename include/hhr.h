@@ -246,6 +246,8 @@ size_t hhr_decode_step_workspace_bytes(const hhr_dims* dims, int m_pages, int ke
  *             seq_len[b] - 1 (its page must be mapped in page_table).
  *   k_new, v_new : bf16 [B][G][d] newest rows, written into k_cache/v_cache at that
  *             position before encoding; both NULL when the caller already wrote them.
+ *             Block means are not written: where they are in use, hhr_encode_keys for the same
+ *             row, with block_mean alone, follows.
  *   opts, out_idx, out_count, out, scale : as in hhr_select / hhr_sparse_attn.
  * workspace: at least hhr_decode_step_workspace_bytes(). Errors as in the separate calls. */
 int hhr_decode_step(const hhr_dims* dims, const uint16_t* q, const uint16_t* k_new,

@@ -249,3 +249,37 @@ def test_a_refused_dense_step_writes_nothing_and_buffers_may_be_larger():
     status_ok()
     assert torch.equal(cache.block_mean, means) and means.any() and int((cache.k_exp != 0).sum()) == B * G
     assert step.newest.start.tolist() == [4, 2]
+
+
+@pytest.mark.parametrize("with_new_rows", [False, True])
+def test_a_fused_step_keeps_the_block_means(with_new_rows):
+    """Tokens appended by fused hash steps to a cache with block means: the means are the encoder's, bit for
+    bit, and the hash metadata and outputs those of a cache without means."""
+    build.build()
+    wl = S.scaled(S.WORKLOADS["llama8b_32k"], batch=2, seq_lens=(300, 170), top_k=64, m_pages=4, keep_div=0)
+    inp = S.make_inputs(wl, device="cuda")
+    d = dims_of(wl, inp)
+    zero, P = i32([0, 0]), wl.page_size
+    caches = [LayerCache(d, "cuda", block_means=True), LayerCache(d, "cuda"), LayerCache(d, "cuda", block_means=True)]
+    steps = [DecodeStep(d, hhr.HHR_MODE_HASH, wl.m_pages, 0, wl.top_k, "cuda") for _ in range(2)]
+    kv = [(inp["k_cache"].clone(), inp["v_cache"].clone()) for _ in range(2)]
+    first = [x - 40 for x in wl.seq_lens]
+    for c in caches[:2]:
+        hhr.hhr_encode_keys(d, inp["k_cache"], inp["page_table"], zero, i32(first), max(first), inp["R"], inp["W"],
+                            c.page_minmax, c.codes, c.block_mean)
+    gen = torch.Generator(device="cuda").manual_seed(29)
+    for t in range(1, 41):
+        n = i32([x + t for x in first])
+        q = torch.randn(2, wl.n_q_heads, D, generator=gen, device="cuda").bfloat16()
+        new = [torch.randn(2, wl.n_kv_heads, D, generator=gen, device="cuda").bfloat16() if with_new_rows else None
+               for _ in "kv"]
+        for step, c, (k, v) in zip(steps, caches, kv):
+            step.fused_step(q, k, v, inp["page_table"], n, inp["R"], inp["W"], c, k_new=new[0], v_new=new[1])
+        status_ok()
+        assert torch.equal(steps[0].out, steps[1].out) and torch.equal(steps[0].idx, steps[1].idx)
+    assert torch.equal(caches[0].codes, caches[1].codes)
+    assert torch.equal(caches[0].page_minmax, caches[1].page_minmax)
+    hhr.hhr_encode_keys(d, kv[0][0], inp["page_table"], zero, n, max(wl.seq_lens), None, None, None, None,
+                        caches[2].block_mean)
+    status_ok()
+    assert torch.equal(caches[0].block_mean, caches[2].block_mean) and caches[0].block_mean.any()
