@@ -26,8 +26,8 @@
 // P is used in parts (bf16: three, f16: two), so that the fp32 output is not limited by the matrix
 // operands' type: 2e-7 to 5e-7 off the 64-bit result at 517 to 128K keys.
 //
-// Measured (B200, calls in a row): 8 x 128K keys x 8 KV heads in bf16 635-640 us, 6.7 TB/s of K and V
-// (the measured copy rate is 6.55); 16 ragged sequences of 8K to 128K keys in 8 bits 409-414 us, 6.1
+// Measured (B200, calls in a row): 8 x 128K keys x 8 KV heads in bf16 633-640 us, 6.7 TB/s of K and V
+// (the measured copy rate is 6.55); 16 ragged sequences of 8K to 128K keys in 8 bits 407-414 us, 6.1
 // TB/s; 1 x 32K keys 30.6 us, of which the stream takes 21; 1 x 517 keys 5.7 us, where the page table
 // is no wider than 4096 keys.
 //

@@ -241,3 +241,92 @@ def test_a_scale_of_zero_keeps_infinite_and_nan_queries(kv8):
     q[0, 1, 5], q[0, 2, 6] = math.nan, -math.inf
     out, lse = run(c, q, "dense", 0.0)
     assert torch.isnan(out[1:3]).all() and torch.isfinite(out[[0, 3]]).all()
+
+
+@pytest.mark.parametrize("pages", [8, 600])
+def test_many_sequences_with_far_rows_new_ones_among_them(pages):
+    """A ragged batch of more sequences than a warp scans, some with far rows, some with a far new row
+    that the call writes; captured once and replayed over other rows."""
+    build.build()
+    P, G, gs, B = 16, 2, 4, 41
+    lens = [(97 * i) % (5 * P) for i in range(B)]
+    lens[7], lens[30] = pages * P, pages * P - 3
+    c = Paged(lens, G, gs, P, True, seed=900, extra_cols=0)
+    q = c.queries(B)
+    kn, vn = (torch.randn(B, G, D, device="cuda").bfloat16() for _ in "kv")
+    vn[3::5, :, 9] = math.inf
+    vn[4::5, 0, 100] = 2.0 ** 60
+    for b in (7, 11, 30):
+        phys, slot = int(c.pt[b, 1]), 5
+        c.v[phys, 0, slot] = 0
+        c.v[phys, 0, slot, 77], c.v_exp[phys, 0, slot] = 0x7e, 190
+    out = torch.full((B, G * gs, D), math.nan, device="cuda")
+    lse = torch.full((B, G * gs), math.nan, device="cuda")
+    ws = torch.full((hhr.hhr_paged_attn_workspace_bytes(c.d),), 0xff, dtype=torch.uint8, device="cuda")
+
+    def call():
+        hhr.hhr_paged_attn(c.d, q, kn, vn, c.k, c.v, c.k_exp, c.v_exp, c.pt, c.seq_len, SCALE, out, ws, lse=lse)
+
+    def verify():
+        status_ok()
+        for b, n in enumerate(lens):
+            pos = torch.arange(n, device="cuda")
+            for g in range(G):
+                h = slice(g * gs, (g + 1) * gs)
+                if n == 0:
+                    assert (out[b, h] == 0).all() and (lse[b, h] == -math.inf).all()
+                    continue
+                o, l, to, tl = ref_rows(q[b, h], c.rows("k", b, g, pos), c.rows("v", b, g, pos), SCALE)
+                check(out[b, h], o, to, f"sequence {b}, KV head {g}")
+                check(lse[b, h], l, tl, f"sequence {b}, KV head {g} lse")
+
+    call()
+    verify()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for far in (0, 1):
+        vn.normal_()
+        if far:
+            vn[::3, 1, 64] = 2.0 ** 90
+        q.normal_()
+        out.fill_(math.nan)
+        graph.replay()
+        verify()
+
+
+@pytest.mark.parametrize("per_head", [False, True])
+@pytest.mark.parametrize("P,m", [(16, 5), (128, 40)])
+def test_a_chunk_of_queries_over_far_rows(P, m, per_head):
+    """Lists of several queries, causal, some of which name a page with a far row."""
+    build.build()
+    lens, G, gs, T = [9000, 400], 2, 4, 3
+    c = Paged(lens, G, gs, P, True, seed=910)
+    c.d.select_per_head = int(per_head)
+    rows = G * gs if per_head else G
+    q = c.queries(2, T)
+    for b, page in ((0, 2), (0, 3000 // P), (1, 0)):
+        phys = int(c.pt[b, page])
+        c.v[phys, :, 3] = 0
+        c.v[phys, :, 3, 50], c.v_exp[phys, :, 3] = 0x7e, 200
+    gen = torch.Generator(device="cuda").manual_seed(911)
+    pages = torch.tensor([-(-n // P) for n in lens], device="cuda")
+    blocks = (torch.rand(2, T, rows, m, generator=gen, device="cuda") * pages[:, None, None, None]).int()
+    blocks[:, 0, :, 1] = 2 if P == 16 else 0
+    count = torch.full((2, T, rows), m, dtype=torch.int32, device="cuda")
+    q_pos = torch.tensor([[n - 300, n - 2, n + 5] for n in lens], dtype=torch.int32, device="cuda")
+    out, lse = torch.full(q.shape, math.nan, device="cuda"), torch.full(q.shape[:-1], math.nan, device="cuda")
+    ws = torch.full((hhr.hhr_block_attn_workspace_bytes(c.d, T, m),), 0xff, dtype=torch.uint8, device="cuda")
+    hhr.hhr_block_attn(c.d, q, c.k, c.v, c.k_exp, c.v_exp, c.pt, c.seq_len, q_pos, blocks, count, SCALE, out, ws,
+                       lse=lse)
+    status_ok()
+    per = G * gs // rows
+    for b, n in enumerate(lens):
+        for t in range(T):
+            for r in range(rows):
+                at = (blocks[b, t, r].long()[:, None] * P + torch.arange(P, device="cuda")).reshape(-1)
+                at = at[at < min(n, int(q_pos[b, t]) + 1)]
+                g, h = r * G // rows, slice(r * per, (r + 1) * per)
+                o, l, to, tl = ref_rows(q[b, t, h], c.rows("k", b, g, at), c.rows("v", b, g, at), SCALE)
+                check(out[b, t, h], o, to, f"sequence {b}, query {t}, row {r}")
+                check(lse[b, t, h], l, tl, f"sequence {b}, query {t}, row {r} lse")
